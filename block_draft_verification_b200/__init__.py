@@ -13,8 +13,8 @@ import torch
 
 __all__ = ["F32", "BF16", "Q_SOFTMAX", "Q_ONEHOT", "K", "DFlash2Error", "lib", "workspace_bytes",
            "Workspace", "topk_softmax", "pair_select", "verify_greedy", "verify_sample",
-           "verify_sample_trunc", "dynconv2", "PackedTap", "status_string", "version",
-           "device_errors"]
+           "verify_sample_trunc", "dynconv2", "PackedTap", "PackedW4", "linear_w4",
+           "status_string", "version", "device_errors"]
 
 F32, BF16 = 0, 1
 Q_SOFTMAX, Q_ONEHOT = 0, 1
@@ -68,13 +68,19 @@ def lib():
         L.dflash2_dynconv2_packed_bytes.restype = sz
         L.dflash2_dynconv2_workspace_bytes.argtypes = [i32, i32, i32, i32]
         L.dflash2_dynconv2_workspace_bytes.restype = sz
+        L.dflash2_w4_packed_bytes.argtypes = [i64, i64, i32, i32]
+        L.dflash2_w4_packed_bytes.restype = sz
+        L.dflash2_w4_pack.argtypes = [vp, vp, vp, i64, i64, i32, i32, vp, vp]
+        L.dflash2_linear_w4.argtypes = [vp, i32, i64, i64, vp, i64, i64, i32, i32, vp, i32, vp]
+        L.dflash2_dynconv2_w4.argtypes = [vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp]
         L.dflash2_device_errors.argtypes = [i32]
         L.dflash2_device_errors.restype = C.c_uint32
         for f in ("dflash2_topk_softmax", "dflash2_topk_softmax_ex", "dflash2_pair_select",
                   "dflash2_pair_select_ex", "dflash2_verify_greedy_early_exit",
                   "dflash2_verify_greedy", "dflash2_verify_sample", "dflash2_verify_sample_ex",
                   "dflash2_verify_sample_trunc", "dflash2_dynconv2", "dflash2_dynconv2_pack",
-                  "dflash2_dynconv2_packed"):
+                  "dflash2_dynconv2_packed", "dflash2_w4_pack", "dflash2_linear_w4",
+                  "dflash2_dynconv2_w4"):
             getattr(L, f).restype = i32
         _lib = L
     return _lib
@@ -334,10 +340,13 @@ class PackedTap:
 
 
 def dynconv2(x, x_prev, w_tap, out=None, ws=None):
-    """x [B, T, H], x_prev [B, H], w_tap [2H, H] (one dtype) or a PackedTap ->
-    out [B, T, H]."""
+    """x [B, T, H], x_prev [B, H], w_tap [2H, H] (one dtype), a PackedTap or a
+    PackedW4(taps=True) -> out [B, T, H].  With 4-bit taps (dflash2_dynconv2_w4)
+    no workspace is used."""
     if isinstance(w_tap, PackedTap):
         return _dynconv2_packed(x, x_prev, w_tap, out, ws)
+    if isinstance(w_tap, PackedW4):
+        return _dynconv2_w4(x, x_prev, w_tap, out)
     _cuda(x, x_prev, w_tap)
     B, T, H = x.shape
     if out is None:
@@ -366,4 +375,107 @@ def _dynconv2_packed(x, x_prev, pk, out, ws):
     _check("dflash2_dynconv2_packed", lib().dflash2_dynconv2_packed(
         _p(x.contiguous()), _p(x_prev.contiguous()), _p(pk.buf), _dtype(x), B, T, H, _p(out), wp,
         wb, _stream(x.device)))
+    return out
+
+
+W4_ZERO, W4_SCALE_F32, W4_TAPS = 1, 2, 4
+
+
+def _call(name, dev, *args):
+    """One library call on the current stream of `dev`, with `dev` current: the
+    library launches on the calling thread's device."""
+    index = dev.index
+    stream = torch._C._cuda_getCurrentRawStream(index)  # current_stream(dev).cuda_stream, without its object
+    f = getattr(_lib or lib(), name)
+    if torch._C._cuda_getDevice() == index:
+        rc = f(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            rc = f(*args, stream)
+    if rc:
+        raise DFlash2Error(name, rc)
+
+
+def _same_device(dev, *ts):
+    for t in ts:
+        if t is not None and t.device != dev:
+            raise ValueError("dflash2 calls take tensors of one CUDA device")
+
+
+class PackedW4:
+    """Weights [N, K] held in 4 bits, packed once (dflash2_w4_pack) for linear_w4
+    or, with taps=True (N = 2K), for dynconv2:
+    W[n, k] = scale[n, k // group] * (q[n, k] - zero[n, k // group]).
+    q [N, K/2] uint8 codes, the even k in the low half of each byte; scale
+    [N, K/group] bfloat16 or float32; zero [N, K/group] uint8 in 0..15, or None
+    for 8 everywhere."""
+
+    def __init__(self, q, scale, zero=None, taps=False):
+        _cuda(q, scale, zero)
+        _same_device(q.device, scale, zero)
+        if q.dtype != torch.uint8 or (zero is not None and zero.dtype != torch.uint8):
+            raise TypeError("4-bit codes and zero points are uint8")
+        if q.dim() != 2 or scale.dim() != 2 or scale.shape[0] != q.shape[0] or \
+                (zero is not None and zero.shape != scale.shape):
+            raise ValueError("expected q [N, K/2], scale and zero [N, K/group]")
+        self.N, self.K = q.shape[0], 2 * q.shape[1]
+        groups = scale.shape[1]
+        if groups < 1 or self.K % groups:
+            raise ValueError("%d groups do not divide K = %d" % (groups, self.K))
+        self.group = self.K // groups
+        self.format = ((W4_ZERO if zero is not None else 0) |
+                       (W4_SCALE_F32 if _dtype(scale) == F32 else 0) | (W4_TAPS if taps else 0))
+        self.taps = bool(taps)
+        self.device = q.device
+        n = int(lib().dflash2_w4_packed_bytes(self.N, self.K, self.group, self.format))
+        self.buf = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+        q, scale = q.contiguous(), scale.contiguous()
+        zero = None if zero is None else zero.contiguous()
+        _call("dflash2_w4_pack", q.device, q.data_ptr(), scale.data_ptr(),
+              None if zero is None else zero.data_ptr(), self.N, self.K, self.group, self.format,
+              self.buf.data_ptr())
+
+
+def linear_w4(x, w4, out_dtype=None, out=None):
+    """x [..., K] float32 or bfloat16 (rows may be strided), w4 a PackedW4 ->
+    y [..., N] of out_dtype (default x's): y = x W^T (dflash2_linear_w4)."""
+    if w4.taps:
+        raise ValueError("weights packed as taps are for dynconv2")
+    K, N = w4.K, w4.N
+    shape = x.shape
+    if shape[-1] != K:
+        raise ValueError("x has %d columns, the weights K = %d" % (shape[-1], K))
+    if not x.is_cuda or x.device != w4.device:
+        raise ValueError("x and the weights are on one CUDA device")
+    x2 = x if x.dim() == 2 else x.reshape(-1, K)
+    rows, stride = x2.shape[0], x2.stride(0)
+    if x2.stride(1) != 1 or (rows > 1 and stride < K):
+        x2 = x2.contiguous()
+        stride = K
+    if out is None:
+        out = torch.empty(shape[:-1] + (N,), dtype=out_dtype or x.dtype, device=x.device)
+    elif out.shape != shape[:-1] + (N,) or not out.is_contiguous() or out.device != x.device or \
+            (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError("out is not a dense [..., N] tensor of the result's type")
+    _call("dflash2_linear_w4", x.device, x2.data_ptr(), _dtype(x), stride if rows > 1 else K, rows,
+          w4.buf.data_ptr(), N, K, w4.group, w4.format, out.data_ptr(), _dtype(out))
+    return out
+
+
+def _dynconv2_w4(x, x_prev, w4, out):
+    if not w4.taps:
+        raise ValueError("dynconv2 takes weights packed with taps=True")
+    if not x.is_cuda or x.device != w4.device or x_prev.device != w4.device:
+        raise ValueError("x, x_prev and the weights are on one CUDA device")
+    B, T, H = x.shape
+    if H != w4.K or x_prev.shape != (B, H) or x_prev.dtype != x.dtype:
+        raise ValueError("expected x [B, T, %d] and x_prev [B, %d] of one dtype" % (w4.K, w4.K))
+    x, x_prev = x.contiguous(), x_prev.contiguous()
+    if out is None:
+        out = torch.empty_like(x)
+    elif out.shape != x.shape or out.dtype != x.dtype or not out.is_contiguous() or \
+            out.device != x.device:
+        raise ValueError("out is not a dense tensor like x")
+    _call("dflash2_dynconv2_w4", x.device, x.data_ptr(), x_prev.data_ptr(), w4.buf.data_ptr(),
+          w4.group, w4.format, _dtype(x), B, T, H, out.data_ptr())
     return out

@@ -15,6 +15,9 @@
  *                          distributions
  *   dflash2_dynconv2       two-tap dynamic depthwise conv fused with its tap
  *                          projection and the residual add
+ *   dflash2_linear_w4      product with weights held in 4 bits with group
+ *                          scales (the drafter's projections and its head)
+ *   dflash2_dynconv2_w4    the conv with its tap weights held the same way
  *
  * Source pages (cited by title and section):
  *   [tamsi]    "DFlash 2 — 3× plus de tokens sur Qwen3.8-27B, même sortie",
@@ -422,6 +425,72 @@ DFLASH2_API int dflash2_dynconv2_pack(const void* w_tap, int dtype, int H, void*
 DFLASH2_API int dflash2_dynconv2_packed(const void* x, const void* x_prev, const void* w_packed,
                                         int dtype, int B, int T, int H, void* out, void* ws,
                                         size_t ws_bytes, dflash2_stream_t stream);
+
+/*
+ * Products with 4-bit weights and group scales, for the few tokens of a decode
+ * step ([latenode] "Preguntas frecuentes": the drafters and targets are served
+ * quantised).  Weights:
+ *
+ *   W[n, k] = scale[n, k / group] * (q[n, k] - zero[n, k / group])
+ *
+ * with codes q in 0..15, K / group scales per row and zero = 8 where no zero
+ * points are given.  A quantiser's output is packed once, dflash2_w4_pack, and
+ * the packed weights serve every token count.
+ *
+ * format      0 for bf16 scales and no zero points, or the sum of
+ *             DFLASH2_W4_ZERO       zero points are given,
+ *             DFLASH2_W4_SCALE_F32  the scales are float,
+ *             DFLASH2_W4_TAPS       the weights are a conv's taps [2H, H] (rows
+ *                                   of a and b stored in turn; N = 2 K and
+ *                                   K a multiple of 64: dflash2_dynconv2_w4).
+ *             Other values: DFLASH2_EINVAL.  Pack and use take the same one.
+ * N           in [1, 2^31 - 1];  K in [32, 2^20], a multiple of group;
+ * group       32 or a multiple of 64 (K itself: one scale per row).
+ *
+ * dflash2_w4_packed_bytes  bytes of the packed form (0 for invalid arguments).
+ * dflash2_w4_pack  q [N, K/2] bytes, the even k in the low half, 16-byte
+ *   aligned; scale [N, K/group] bf16 or float; zero [N, K/group] bytes, given
+ *   exactly when the format says so (DFLASH2_EINVAL otherwise); packed 256-byte
+ *   aligned.  One launch on `stream`.  A zero point above 15 counts as 15 and
+ *   sets device error flag 32.  The layout is internal.
+ */
+#define DFLASH2_W4_ZERO 1
+#define DFLASH2_W4_SCALE_F32 2
+#define DFLASH2_W4_TAPS 4
+DFLASH2_API size_t dflash2_w4_packed_bytes(int64_t N, int64_t K, int group, int format);
+DFLASH2_API int dflash2_w4_pack(const uint8_t* q, const void* scale, const uint8_t* zero,
+                                int64_t N, int64_t K, int group, int format, void* packed,
+                                dflash2_stream_t stream);
+
+/*
+ * y[t, n] = sum_k W[n, k] x[t, k].
+ * x           [tokens, x_stride] of `dtype` (x_stride >= K elements; columns
+ *             K .. x_stride - 1 unused); rows that start on 16 bytes are read
+ *             with 128-bit loads, others element by element.
+ * tokens      in [0, 2^18] (0 is a no-op).
+ * packed      from dflash2_w4_pack for the same N, K, group and format
+ *             (without DFLASH2_W4_TAPS).
+ * y           [tokens, N] of `out_dtype`, dense.
+ * The codes minus their zero points are multiplied exactly (fp32 activations
+ * as three bf16 parts that add up to the value), sums are fp32, with one
+ * rounding at a bf16 output; |x| below 2^-100 may lose its last bits.  A
+ * given shape on a given device always rounds the same way; a token's last
+ * bits may depend on how many tokens the call has.  No workspace: calls may
+ * run at the same time on any streams.
+ */
+DFLASH2_API int dflash2_linear_w4(const void* x, int dtype, int64_t x_stride, int64_t tokens,
+                                  const void* packed, int64_t N, int64_t K, int group, int format,
+                                  void* y, int out_dtype, dflash2_stream_t stream);
+
+/*
+ * dflash2_dynconv2 with the tap weights in 4 bits: `packed` from
+ * dflash2_w4_pack with N = 2H, K = H and DFLASH2_W4_TAPS in `format`.  x, x_prev
+ * and out as in dflash2_dynconv2, both dtypes; B * T <= 2^18; sums and
+ * workspace as in dflash2_linear_w4.
+ */
+DFLASH2_API int dflash2_dynconv2_w4(const void* x, const void* x_prev, const void* packed,
+                                    int group, int format, int dtype, int B, int T, int H,
+                                    void* out, dflash2_stream_t stream);
 
 /*
  * Device-side error flags of the kernels on the current device (0 = none).

@@ -58,6 +58,7 @@ def _sig():
     L.orc_verify_sample_trunc.argtypes = [vp, vp, i32, i32, i32, i64, vp, dbl, i32, dbl, u64,
                                           u32, vp, i32, vp, vp, vp, vp, vp, vp, vp]
     L.orc_dynconv2.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp]
+    L.orc_linear_w4.argtypes = [vp, i32, i64, vp, vp, i32, vp, i64, i64, i64, vp, vp]
 
 
 def _dtype_of(a):
@@ -268,3 +269,31 @@ def dynconv2(x, x_prev, w_tap):
     out = np.zeros((B, T, H), np.float64)
     _check(lib().orc_dynconv2(_p(xx), _p(xp), _p(w), dt, B, T, H, _p(out)), "dynconv2")
     return out
+
+
+# ---------------------------------------------------------------- 4-bit weights
+def linear_w4(x, q, scale, zero=None):
+    """x [tokens, K], q [N, K/2] uint8 (even k in the low half), scale [N, K/group],
+    zero [N, K/group] uint8 or None -> y [tokens, N] f64, sum of |products| f64."""
+    xx, qq, ss = np.ascontiguousarray(x), _c(q, np.uint8), np.ascontiguousarray(scale)
+    zz = None if zero is None else _c(zero, np.uint8)
+    tokens, K = xx.shape
+    N = qq.shape[0]
+    y, mag = np.zeros((tokens, N), np.float64), np.zeros((tokens, N), np.float64)
+    _check(lib().orc_linear_w4(_p(xx), _dtype_of(xx), tokens, _p(qq), _p(ss), _dtype_of(ss),
+                               _p(zz), N, K, K // ss.shape[1], _p(y), _p(mag)), "linear_w4")
+    return y, mag
+
+
+def dynconv2_w4(x, x_prev, q, scale, zero=None):
+    """The two-tap conv with the tap weights [2H, H] in 4 bits -> out [B, T, H] f64 and
+    the magnitude |x| + sum |a-products| |x| + sum |b-products| |x_prev| it was summed from."""
+    def f64(a):
+        return ((a.astype(np.uint32) << 16).view(np.float32) if a.dtype == np.uint16 else a).astype(np.float64)
+    B, T, H = x.shape
+    y, mag = linear_w4(np.ascontiguousarray(x).reshape(B * T, H), q, scale, zero)
+    y, mag = y.reshape(B, T, 2, H), mag.reshape(B, T, 2, H)
+    cur = f64(x)
+    prev = np.concatenate([f64(x_prev)[:, None], cur[:, :-1]], axis=1)
+    return (cur + y[:, :, 0] * cur + y[:, :, 1] * prev,
+            np.abs(cur) + mag[:, :, 0] * np.abs(cur) + mag[:, :, 1] * np.abs(prev))

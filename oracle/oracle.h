@@ -110,6 +110,12 @@ int orc_verify_sample_trunc(const void* target, const void* draft, int dtype, in
 int orc_dynconv2(const void* x, const void* x_prev, const void* w_tap, int dtype,
                  int B, int T, int H, double* out);
 
+/* ---- product with 4-bit weights and group scales: y [tokens, N] and,
+ *      optionally, the sums of the products' magnitudes ---- */
+int orc_linear_w4(const void* x, int dtype, int64_t tokens, const uint8_t* q, const void* scale,
+                  int scale_dtype, const uint8_t* zero, int64_t N, int64_t K, int64_t group,
+                  double* y, double* abs_sum);
+
 #ifdef __cplusplus
 }
 #endif
