@@ -36,26 +36,48 @@ constexpr int W4_THREADS = 32 * W4_WARPS;
 constexpr int W4_SMEM = 224 * 1024;  // dynamic shared memory a CTA may take
 
 struct W4Args {
-    const uint8_t* weights;
-    const uint8_t* scales;
+    const uint8_t* packed;
     int64_t N, K, units, tokens;
-    int chunks, groups, group;
     const void* x;
     int64_t x_stride;
     int x_vec;           // rows of x start on 16 bytes
-    int gdiv;            // chunks per group, and the reciprocal that divides by it
-    uint32_t gmagic;
     void* y;             // linear: [tokens, N] in y_bf16's type; conv: [tokens, H] in x's
     int y_bf16;
     const void* x_prev;  // conv; NULL: linear
     int T;               // conv: tokens per sequence
     // plan
     int S, C;            // cluster size, clusters
+    int steps;           // of K, one or two chunks each
     int tile;            // tokens per tile (8 NT at most)
-    int phase, phases;   // chunks of x in shared memory at a time, and how often
+    int phase, phases;   // steps of x in shared memory at a time, and how often
     int batch;           // units whose sums are in shared memory at a time
     int slots;           // partial sums per unit
+    int x_off, xsum_off, part_off, counts_off;  // byte offsets in shared memory
 };
+
+// Shared memory of a step in a warp's ring: the lanes' 16-byte pieces of its
+// chunks, then every lane's scales.  Lanes copy (and read) their own pieces
+// only, so a warp's ring needs no barrier.
+__host__ __device__ constexpr int w4_stage_bytes(int kb, int sg, int fmt) {
+    return kb * W4_CHUNK_BYTES + sg * 32 * (w4_scale_bytes(fmt) / 8);
+}
+// Steps in the ring: what fits 7.5 KB a warp, two at least.
+__host__ __device__ constexpr int w4_stages(int kb, int sg, int fmt) {
+    const int n = 7680 / w4_stage_bytes(kb, sg, fmt);
+    return n < 2 ? 2 : n;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 __device__ __forceinline__ void store_out(void* y, int64_t i, float v, bool bf16) {
     if (bf16)
@@ -124,27 +146,37 @@ __device__ __forceinline__ void load_x8(const XT* row, int64_t k, int64_t K, boo
 }
 
 // XT: activation type; NT: 8-token tiles; FMT: scale format; G32: groups of
-// 32 (two per chunk).
-template <typename XT, int NT, int FMT, bool G32>
+// 32 (two per chunk); KB: chunks per step (2 where the group is a multiple of
+// 128: one scaling, one set of loads and one turn of the loop for 128 k);
+// OFFS: codes to operands by offset (w4.cuh).
+template <typename XT, int NT, int FMT, bool G32, int KB, bool OFFS>
 __global__ void __launch_bounds__(W4_THREADS, 1) linear_w4_kernel(const W4Args a) {
+    static_assert(!(G32 && KB > 1), "groups of 32 end inside a chunk");
     constexpr int NP = sizeof(XT) == 4 ? 3 : 1;
-    constexpr int D = NT <= 2 ? 4 : 2;  // items in flight per warp
-    constexpr int SG = G32 ? 2 : 1;
+    constexpr int SG = G32 ? 2 : 1;  // scale groups per step
+    constexpr int LB = W4Scale<FMT>::BYTES;
+    constexpr int STAGE = w4_stage_bytes(KB, SG, FMT), D = w4_stages(KB, SG, FMT);
+    constexpr int STEP = KB * W4_CHUNK_BYTES + SG * w4_scale_bytes(FMT);  // packed bytes
     extern __shared__ __align__(16) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = blockIdx.x % a.S, cl = blockIdx.x / a.S;
     const int64_t tok0 = (int64_t)blockIdx.y * a.tile;
     const int nt = (int)min((int64_t)a.tile, a.tokens - tok0);
 
-    const int ck0 = (int)((int64_t)a.chunks * rank / a.S);
-    const int ck1 = (int)((int64_t)a.chunks * (rank + 1) / a.S);
+    // this CTA's steps of K and units
+    const int k0 = a.steps * rank / a.S, k1 = a.steps * (rank + 1) / a.S;
     const int64_t u0 = a.units * cl / a.C, u1 = a.units * (cl + 1) / a.C;
 
-    // shared memory: x [chunk][half][plane][token][32 k] bf16 (64-byte rows),
-    // then the partial sums [unit of the batch][slot][NT * 8][32 lanes] fp32
+    // shared memory: the warps' rings, x [chunk][half][plane][token][32 k] bf16
+    // (64-byte rows), the sums of x [step][group of the step][8 NT tokens]
+    // (OFFS), then the partial sums [unit of the batch][slot][NT * 8][32 lanes]
+    // fp32 and the units' slot counts
     const int xrow = nt * 64, xchunk = 2 * NP * xrow;
-    uint8_t* xs = smem;
-    float* part = (float*)(smem + (size_t)a.phase * 2 * NP * a.tile * 64);
+    uint8_t* ring = smem + warp * (D * STAGE);
+    const uint32_t ring_u = smem_u32(ring) + lane * 16, ring_s = smem_u32(ring) + KB * W4_CHUNK_BYTES + lane * LB;
+    uint8_t* xs = smem + a.x_off;
+    float* xsum = (float*)(smem + a.xsum_off);
+    float* part = (float*)(smem + a.part_off);
     constexpr int PU = NT * 8 * 32;  // floats of one slot
 
     const int phases = a.phases;
@@ -152,63 +184,113 @@ __global__ void __launch_bounds__(W4_THREADS, 1) linear_w4_kernel(const W4Args a
     // n items are cut into min(warps, n) runs, none empty: run w is items
     // n w / R .. n (w + 1) / R - 1, so a unit's items lie in adjacent runs and
     // run w fills slot w - (the run of the unit's first item).
-    auto runs_of = [](int64_t n) { return (int)min((int64_t)W4_WARPS, n); };
-    auto run_of = [&](int64_t i, int64_t n) { return (int)(((i + 1) * runs_of(n) - 1) / n); };
+    // (n is at most 2^24, batch x steps of a phase)
+    auto runs_of = [](int n) { return min(W4_WARPS, n); };
+    auto run_of = [&](int i, int n) { return (int)((unsigned)((i + 1) * runs_of(n) - 1) / (unsigned)n); };
 
+    // The run at hand, of batch ub and phase ph: its items are cu, cc (unit and
+    // step) onward; `left` of them are not yet requested.
+    int c0 = 0, nc = 0, n = 0, cu = 0, cc = 0, len = 0, left = 0, lc = 0, st_load = 0, st_read = 0;
+    const uint8_t* lw = nullptr;
+    auto request = [&]() {  // the next step into the ring (an empty group at the run's end)
+        if (left > 0) {
+            --left;
+            const uint32_t dst = ring_u + st_load * STAGE;
+            const uint8_t* src = lw + lane * 16;
+#pragma unroll
+            for (int q = 0; q < 2 * KB; ++q) cp_async16(dst + q * 512, src + q * 512);
+            const uint32_t dsc = ring_s + st_load * STAGE;
+            const uint8_t* ssc = lw + KB * W4_CHUNK_BYTES + (lane >> 2) * LB;
+#pragma unroll
+            for (int h = 0; h < SG; ++h) {
+                if constexpr (LB == 8) {
+                    cp_async8(dsc + h * 32 * LB, ssc + h * 8 * LB);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < LB / 16; ++q)
+                        cp_async16(dsc + h * 32 * LB + 16 * q, ssc + h * 8 * LB + 16 * q);
+                }
+            }
+            st_load = st_load + 1 == D ? 0 : st_load + 1;
+            lw += STEP;
+            if (++lc == nc) {
+                lc = 0;
+                lw += (int64_t)(a.steps - nc) * STEP;
+            }
+        }
+        cp_async_commit();
+    };
+    auto start = [&](int64_t ub, int ph) {
+        const int nu = (int)min((int64_t)a.batch, u1 - ub);
+        c0 = k0 + ph * a.phase;
+        nc = max(0, min(a.phase, k1 - c0));
+        n = nu * nc;
+        const int runs = runs_of(n);
+        const int i0 = warp < runs ? (int)((unsigned)(n * warp) / (unsigned)runs) : 0;
+        const int i1 = warp < runs ? (int)((unsigned)(n * (warp + 1)) / (unsigned)runs) : 0;
+        left = len = i1 - i0;
+        cu = nc > 0 ? i0 / nc : 0;
+        lc = cc = i0 - cu * nc;
+        lw = a.packed + ((ub + cu) * a.steps + c0 + cc) * STEP;
+        st_load = st_read = 0;
+#pragma unroll
+        for (int d = 0; d < D - 1; ++d) request();
+    };
+
+    start(u0, 0);
     for (int64_t ub = u0; ub < u1; ub += a.batch) {
         const int nu = (int)min((int64_t)a.batch, u1 - ub);
         for (int ph = 0; ph < phases; ++ph) {
-            const int c0 = ck0 + ph * a.phase, nc = max(0, min(a.phase, ck1 - c0));
-            const int64_t n = (int64_t)nu * nc;
-            const int runs = runs_of(n);
-            const int i0 = warp < runs ? (int)(n * warp / runs) : 0;
-            const int i1 = warp < runs ? (int)(n * (warp + 1) / runs) : 0;
-
-            // the run's first items are on their way while x is laid out
-            uint4 wb[D][2];
-            W4Scale<FMT> sb[D][SG];
-            int lu = 0, lc = 0;  // unit and chunk of the next item to load
-            if (nc > 0) {
-                lu = i0 / nc;
-                lc = i0 - lu * nc;
-            }
-            auto load = [&](int d) {
-                const int64_t u = ub + lu;
-                const int c = c0 + lc;
-                const uint4* p = (const uint4*)(a.weights + (u * a.chunks + c) * W4_BLOCK) + lane;
-                wb[d][0] = __ldcs(p);
-                wb[d][1] = __ldcs(p + 32);
-                const int g = G32 ? 2 * c : a.gdiv == 1 ? c : (int)__umulhi((unsigned)c, a.gmagic);
-                const uint8_t* s = a.scales + (u * a.groups + g) * w4_scale_bytes(FMT);
-#pragma unroll
-                for (int h = 0; h < SG; ++h) sb[d][h].load(s + h * w4_scale_bytes(FMT), lane >> 2);
-                if (++lc == nc) {
-                    lc = 0;
-                    ++lu;
-                }
-            };
-#pragma unroll
-            for (int d = 0; d < D; ++d)
-                if (i0 + d < i1) load(d);
-
             // x of this phase (kept over the batches when there is one phase)
-            if (phases > 1 || ub == u0) {
-                const int items = nc * 8 * nt;  // (chunk, half, 8 k) per token
+            const bool new_x = phases > 1 || ub == u0;
+            if (new_x) {
+                const int items = nc * KB * 8 * nt;  // (chunk, half, 8 k) per token
                 for (int i = threadIdx.x; i < items; i += W4_THREADS) {
                     const int c8 = i & 3, r = i >> 2;
-                    const int t = r % nt, ch = r / nt;  // ch = 2 * chunk + half
+                    const int ch = r / nt, t = r - ch * nt;  // ch = 2 * chunk + half
                     const XT* row = (const XT*)a.x + (tok0 + t) * a.x_stride;
                     uint4 v[NP];
-                    load_x8<XT, NP>(row, (int64_t)(2 * c0 + ch) * 32 + 8 * c8, a.K, a.x_vec != 0, v);
+                    load_x8<XT, NP>(row, (int64_t)(2 * KB * c0 + ch) * 32 + 8 * c8, a.K, a.x_vec != 0, v);
 #pragma unroll
                     for (int p = 0; p < NP; ++p)
                         *(uint4*)(xs + (size_t)(ch * NP + p) * xrow + t * 64 + c8 * 16) = v[p];
                 }
+                if (phases > 1 && ph == 0)
+                    for (int i = threadIdx.x; i < nu * a.slots * PU; i += W4_THREADS) part[i] = 0.0f;
+                __syncthreads();
             }
-            if (phases > 1 && ph == 0)
-                for (int i = threadIdx.x; i < nu * a.slots * PU; i += W4_THREADS) part[i] = 0.0f;
-            __syncthreads();
+            if constexpr (OFFS) {
+                // sums of x over each group's part of a step: four lanes per token
+                if (new_x) {
+                    constexpr int HALVES = 2 * KB / SG;  // 32-k rows per sum
+                    const int items = nc * SG * 8 * NT * 4;
+                    for (int i = threadIdx.x; i < items; i += W4_THREADS) {
+                        const int c8 = i & 3, r = i >> 2, t = r % (8 * NT), pc = r / (8 * NT);
+                        float v = 0.0f;
+                        if (t < nt) {
+#pragma unroll
+                            for (int h = 0; h < HALVES; ++h) {
+                                const uint4 q = *(const uint4*)(xs + (size_t)(pc * HALVES + h) * xrow +
+                                                                t * 64 + c8 * 16);
+                                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    v += __uint_as_float(w[e] << 16) + __uint_as_float(w[e] & 0xFFFF0000u);
+                            }
+                        }
+                        v += __shfl_xor_sync(FULL, v, 1);  // items is a multiple of 32: whole warps
+                        v += __shfl_xor_sync(FULL, v, 2);
+                        if (c8 == 0) xsum[r] = v;
+                    }
+                    __syncthreads();
+                }
+            }
 
+            // a lane's rows of x: tokens past the tile's last read that one's, and
+            // their columns of the products are never looked at
+            uint32_t xoff[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) xoff[t] = min(8 * t + (lane >> 2), nt - 1) * 64 + (lane & 3) * 16;
             float acc[2][NT][4];
 #pragma unroll
             for (int b = 0; b < 2; ++b)
@@ -216,113 +298,126 @@ __global__ void __launch_bounds__(W4_THREADS, 1) linear_w4_kernel(const W4Args a
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) acc[b][t][j] = 0.0f;
-            int cu = 0, cc = 0;  // unit and chunk of the item at hand
-            if (nc > 0) {
-                cu = i0 / nc;
-                cc = i0 - cu * nc;
-            }
-            for (int i = i0; i < i1; i += D) {
+            for (int i = 0; i < len; ++i) {
+                cp_async_wait<D - 2>();
+                const uint8_t* sp = ring + st_read * STAGE;
+                st_read = st_read + 1 == D ? 0 : st_read + 1;
+                request();  // into the stage that the step before this one has left
+                W4Scale<FMT> w4s[SG];
 #pragma unroll
-                for (int d = 0; d < D; ++d) {
-                    if (i + d < i1) {
-                        // operands of the 16-row halves: [half b][k step][4]
-                        uint32_t A[2][4][4];
+                for (int h = 0; h < SG; ++h) w4s[h].load(sp + KB * W4_CHUNK_BYTES + (h * 32 + lane) * LB);
+                uint4 wv[KB][2];
 #pragma unroll
-                        for (int b = 0; b < 2; ++b) {
-                            const uint32_t w[4] = {wb[d][b].x, wb[d][b].y, wb[d][b].z, wb[d][b].w};
+                for (int c = 0; c < KB; ++c)
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const W4Scale<FMT>& s = sb[d][G32 ? h : 0];
-                                const uint32_t zl = s.zero2(2 * b), zh = s.zero2(2 * b + 1);
+                    for (int b = 0; b < 2; ++b)
+                        wv[c][b] = *(const uint4*)(sp + c * W4_CHUNK_BYTES + b * 512 + lane * 16);
+                float s[2][NT][4];
+                const uint8_t* xc = xs + (size_t)cc * KB * xchunk;
+                const float* xq = xsum + (size_t)cc * SG * 8 * NT + 2 * (lane & 3);
 #pragma unroll
-                                for (int q = 0; q < 2; ++q) {
-                                    A[b][2 * h + q][0] = w4_pair(w[h], 2 * q, zl);
-                                    A[b][2 * h + q][1] = w4_pair(w[2 + h], 2 * q, zh);
-                                    A[b][2 * h + q][2] = w4_pair(w[h], 2 * q + 1, zl);
-                                    A[b][2 * h + q][3] = w4_pair(w[2 + h], 2 * q + 1, zh);
-                                }
-                            }
-                        }
-                        float sc[SG][4];
-#pragma unroll
-                        for (int h = 0; h < SG; ++h)
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) sc[h][j] = sb[d][h].scale(j);
-                        if (i + d + D < i1) load(d);
-                        const uint8_t* xc = xs + (size_t)cc * xchunk + lane * 16;
+                for (int h = 0; h < 2 * KB; ++h) {  // 32 k each: two matrix steps
+                    const W4Scale<FMT>& ws = w4s[G32 ? h : 0];
+                    if (h == 0 || G32) {
+                        // the sums start (at zero, or at minus the offset's share)
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
-                            const bool live = 8 * t + (lane >> 2) < nt;
-                            float s[2][4];
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                if (h == 0 || G32)
-#pragma unroll
-                                    for (int b = 0; b < 2; ++b)
-#pragma unroll
-                                        for (int j = 0; j < 4; ++j) s[b][j] = 0.0f;
-#pragma unroll
-                                for (int p = 0; p < NP; ++p) {
-                                    uint4 xv = make_uint4(0, 0, 0, 0);
-                                    if (live)
-                                        xv = *(const uint4*)(xc + (h * NP + p) * xrow + t * 512);
-#pragma unroll
-                                    for (int b = 0; b < 2; ++b) {
-                                        mma_16816(s[b], A[b][2 * h], xv.x, xv.y);
-                                        mma_16816(s[b], A[b][2 * h + 1], xv.z, xv.w);
-                                    }
-                                }
-                                if (h == 1 || G32)
-#pragma unroll
-                                    for (int b = 0; b < 2; ++b)
-#pragma unroll
-                                        for (int j = 0; j < 4; ++j)
-                                            acc[b][t][j] = fmaf(sc[G32 ? h : 0][2 * b + (j >> 1)],
-                                                                s[b][j], acc[b][t][j]);
-                            }
-                        }
-                        if (++cc == nc || i + d + 1 == i1) {
-                            // the run leaves the unit: its sum into the run's slot
-                            const int first = run_of((int64_t)cu * nc, n);
-                            float* p = part + ((size_t)cu * a.slots + (warp - first)) * PU + lane;
+                            float2 q = make_float2(0.0f, 0.0f);
+                            if constexpr (OFFS) q = *(const float2*)(xq + (G32 ? h : 0) * 8 * NT + 8 * t);
 #pragma unroll
                             for (int b = 0; b < 2; ++b)
 #pragma unroll
-                                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                                    for (int j = 0; j < 4; ++j) {
-                                        float* q = p + ((b * NT + t) * 4 + j) * 32;
-                                        *q = phases > 1 ? *q + acc[b][t][j] : acc[b][t][j];
-                                        acc[b][t][j] = 0.0f;
-                                    }
-                            cc = 0;
-                            ++cu;
+                                for (int j = 0; j < 4; ++j)
+                                    s[b][t][j] =
+                                        OFFS ? -ws.zero16(2 * b + (j >> 1)) * ((j & 1) ? q.y : q.x) : 0.0f;
                         }
                     }
+                    uint32_t A[2][2][4];  // [16-row half][matrix step]
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const uint4& w = wv[h >> 1][b];
+                        const uint32_t wl = (h & 1) ? w.y : w.x, wh = (h & 1) ? w.w : w.z;
+#pragma unroll
+                        for (int q = 0; q < 2; ++q)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                if constexpr (OFFS) {
+                                    A[b][q][2 * e] = w4_pair_offset(wl, 2 * q + e);
+                                    A[b][q][2 * e + 1] = w4_pair_offset(wh, 2 * q + e);
+                                } else {
+                                    A[b][q][2 * e] = w4_pair_exact(wl, 2 * q + e, ws.zero2(2 * b));
+                                    A[b][q][2 * e + 1] = w4_pair_exact(wh, 2 * q + e, ws.zero2(2 * b + 1));
+                                }
+                            }
+                    }
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                        for (int p = 0; p < NP; ++p) {
+                            const uint4 xv = *(const uint4*)(xc + (h * NP + p) * xrow + xoff[t]);
+#pragma unroll
+                            for (int b = 0; b < 2; ++b) mma_16816(s[b][t], A[b][0], xv.x, xv.y);
+#pragma unroll
+                            for (int b = 0; b < 2; ++b) mma_16816(s[b][t], A[b][1], xv.z, xv.w);
+                        }
+                        if (h == 2 * KB - 1 || G32)
+#pragma unroll
+                            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    acc[b][t][j] = fmaf(ws.scale(2 * b + (j >> 1)), s[b][t][j], acc[b][t][j]);
+                    }
+                }
+                if (++cc == nc || i + 1 == len) {
+                    // the run leaves the unit: its sum into the run's slot
+                    const int first = run_of(cu * nc, n);
+                    float* p = part + ((size_t)cu * a.slots + (warp - first)) * PU + lane;
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                float* q = p + ((b * NT + t) * 4 + j) * 32;
+                                *q = phases > 1 ? *q + acc[b][t][j] : acc[b][t][j];
+                                acc[b][t][j] = 0.0f;
+                            }
+                    cc = 0;
+                    ++cu;
                 }
             }
-            if (ph + 1 < phases) __syncthreads();  // x is replaced
+            // the next run's first steps are on their way while this one is wound up
+            if (ph + 1 < phases) {
+                start(ub, ph + 1);
+                __syncthreads();  // x is replaced
+            } else if (ub + a.batch < u1) {
+                start(ub + a.batch, 0);
+            }
         }
 
         // Sums of the batch: over the slots and then the cluster, in K order;
-        // this CTA takes every S-th unit.
+        // this CTA takes every S-th unit.  How many slots a unit has in CTA r
+        // is worked out once per unit.
+        uint8_t* counts = smem + a.counts_off;  // [S][batch]
+        for (int i = threadIdx.x; i < a.S * nu; i += W4_THREADS) {
+            const int r = i / nu, j = i - r * nu;
+            int m = a.slots;
+            if (phases == 1) {
+                const int nc = a.steps * (r + 1) / a.S - a.steps * r / a.S;
+                m = run_of(j * nc + nc - 1, nu * nc) - run_of(j * nc, nu * nc) + 1;
+            }
+            counts[r * a.batch + j] = (uint8_t)m;
+        }
         if (a.S > 1)
             cg::this_cluster().sync();
         else
             __syncthreads();
         auto unit_sum = [&](int j, int off) {  // off: position within the slot
             float v = 0.0f;
+            const float* own = part + (size_t)j * a.slots * PU + off;
             for (int r = 0; r < a.S; ++r) {
-                const float* base = a.S > 1 ? cg::this_cluster().map_shared_rank(part, r) : part;
-                int m = a.slots;
-                const int nc = (int)((int64_t)a.chunks * (r + 1) / a.S) -
-                               (int)((int64_t)a.chunks * r / a.S);
-                if (phases == 1) {
-                    const int64_t n = (int64_t)nu * nc;
-                    m = nc > 0 ? run_of((int64_t)j * nc + nc - 1, n) - run_of((int64_t)j * nc, n) + 1
-                               : 0;
-                }
-                base += (size_t)j * a.slots * PU + off;
+                const float* base = a.S > 1 ? cg::this_cluster().map_shared_rank(own, r) : own;
+                const int m = counts[r * a.batch + j];
                 for (int q = 0; q < m; ++q) v += base[(size_t)q * PU];
             }
             return v;
@@ -342,13 +437,14 @@ __global__ void __launch_bounds__(W4_THREADS, 1) linear_w4_kernel(const W4Args a
                 if (nn < a.N) store_out(a.y, (tok0 + t) * a.N + nn, v, a.y_bf16 != 0);
             }
         } else {
-            // rows 0..15 of a unit are a, rows 16..31 b of the same 16 channels
+            // rows 0..7 of a unit's halves are a, rows 8..15 b of the same 8 channels
             const XT* x = (const XT*)a.x;
             for (int i = threadIdx.x; i < mine * nt * 16; i += W4_THREADS) {
                 const int c = i & 15, r = i >> 4, t = r % nt, j = (r / nt) * a.S + rank;
                 const int64_t ch = (ub + j) * 16 + c, tok = tok0 + t;
-                const float av = unit_sum(j, slot_pos(c, t));
-                const float bv = unit_sum(j, slot_pos(16 + c, t));
+                const int ra = (c & 8) * 2 + (c & 7);
+                const float av = unit_sum(j, slot_pos(ra, t));
+                const float bv = unit_sum(j, slot_pos(ra + 8, t));
                 const float xc = to_f32(x[tok * a.K + ch]);
                 const float xp = to_f32(tok % a.T == 0 ? ((const XT*)a.x_prev)[tok / a.T * a.K + ch]
                                                        : x[(tok - 1) * a.K + ch]);
@@ -374,10 +470,11 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const uint8_t* __restrict_
                                                       uint8_t* __restrict__ packed) {
     const bool taps = (format & DFLASH2_W4_TAPS) != 0;
     const bool f32s = (format & DFLASH2_W4_SCALE_F32) != 0;
+    const int sbytes = w4_scale_bytes(format);
     const int64_t kg = L.K / L.group;  // groups per row as given
-    // packed row -> row as given (taps: 16 rows of a, the same 16 of b)
+    // packed row -> row as given (taps: 8 rows of a, the same 8 of b)
     auto source = [&](int64_t r) {
-        return taps ? (r / 32) * 16 + (r & 15) + ((r & 16) ? L.N / 2 : 0) : r;
+        return taps ? (r / 16) * 8 + (r & 7) + ((r & 8) ? L.N / 2 : 0) : r;
     };
     auto zero_at = [&](int64_t row, int64_t g) -> uint32_t {
         if (!zero) return 8u;
@@ -385,43 +482,43 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const uint8_t* __restrict_
         if (z > 15u) atomicOr(&g_dev_err, (unsigned)ERR_INPUT);
         return min(z, 15u);
     };
-    const int64_t nv = L.units * L.chunks * (W4_BLOCK / 16);
-    const int64_t ns = L.units * L.groups * W4_UNIT;
+    const int64_t blocks = L.units * L.steps;
+    const int vecs = L.kb * (W4_CHUNK_BYTES / 16);  // per block
+    const int64_t nv = blocks * vecs, ns = blocks * L.sg * W4_UNIT;
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < nv + ns;
          i += (int64_t)gridDim.x * blockDim.x) {
         if (i < nv) {
-            const int64_t blk = i >> 6;
-            const int v = (int)(i & 63), b = v >> 5, lane = v & 31;
-            const int64_t u = blk / L.chunks;
-            const int c = (int)(blk - u * L.chunks);
+            const int64_t blk = i / vecs, u = blk / L.steps;
+            const int v = (int)(i - blk * vecs), b = (v >> 5) & 1, lane = v & 31;
+            const int64_t c = (blk - u * L.steps) * L.kb + (v >> 6);
             uint32_t w[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {  // row r or r + 8, half h
                 const int64_t row = u * W4_UNIT + 16 * b + (lane >> 2) + 8 * (j >> 1);
-                const int64_t k = (int64_t)c * W4_CHUNK + 32 * (j & 1) + 8 * (lane & 3);
+                const int64_t k = c * W4_CHUNK + 32 * (j & 1) + 8 * (lane & 3);
                 if (row < L.N && k < L.K) {
-                    const int64_t src = source(row);
-                    const uint32_t in = *(const uint32_t*)(q + (src * L.K + k) / 2);
+                    const uint32_t in = *(const uint32_t*)(q + (source(row) * L.K + k) / 2);
                     uint32_t o = 0;
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         o |= ((in >> (4 * e)) & 15u) << (4 * ((e >> 1) + 4 * (e & 1)));
-                    w[j] = o;
+                    w[j] = (o << 3) | (o >> 29);
                 } else {
-                    // K tail: codes equal to the zero point of the group that the
-                    // chunk's first half is scaled with (groups of 32 have scale 0 there)
-                    w[j] = 0x88888888u;
+                    w[j] = 0x44444444u;  // eight codes of 8, turned by three bits
                 }
             }
-            *(uint4*)(packed + blk * W4_BLOCK + v * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+            *(uint4*)(packed + blk * L.step_bytes + v * 16) = make_uint4(w[0], w[1], w[2], w[3]);
         } else {
             const int64_t e = i - nv;
             const int j = (int)(e & 3), g8 = (int)((e >> 2) & 7);  // row = 8 j + g8
-            const int64_t ug = e >> 5, u = ug / L.groups, g = ug - u * L.groups;
+            const int64_t bg = e >> 5, blk = bg / L.sg, u = blk / L.steps;
+            const int h = (int)(bg - blk * L.sg);
             const int64_t row = u * W4_UNIT + 8 * j + g8;
+            const int64_t g = ((blk - u * L.steps) * L.kb * W4_CHUNK + 32 * h) / L.group;
             const bool in = row < L.N && g < kg;
             const int64_t src = in ? source(row) * kg + g : 0;
-            uint8_t* dst = packed + L.scale_off + ug * L.sbytes + (size_t)g8 * (L.sbytes / 8);
+            uint8_t* dst = packed + blk * L.step_bytes + L.kb * W4_CHUNK_BYTES + h * sbytes +
+                           (size_t)g8 * (sbytes / 8);
             const unsigned short z16 =
                 (unsigned short)(0x4300u + (in ? zero_at(source(row), g) : 8u));
             if (f32s) {
@@ -443,44 +540,93 @@ using namespace dfl_host;
 
 namespace {
 
+// The device at hand and how many clusters of each size it holds at once, one
+// CTA per SM (of 148 SMs: 148, 74, 33 and 15 of size 1, 2, 4 and 8; larger
+// clusters fit a GPU's processing clusters less well).
 struct Dev {
-    int id, sms;
+    int id;
+    int clusters[9];
 };
 bool device_info(Dev& d) {
-    return cudaGetDevice(&d.id) == cudaSuccess &&
-           cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, d.id) == cudaSuccess;
+    static std::mutex mu;
+    static Dev known[64] = {};
+    if (cudaGetDevice(&d.id) != cudaSuccess) return false;
+    std::lock_guard<std::mutex> g(mu);
+    if (d.id < 64 && known[d.id].clusters[1] > 0) {
+        d = known[d.id];
+        return true;
+    }
+    auto* k = linear_w4_kernel<__nv_bfloat16, 1, 0, false, 1, true>;
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, W4_SMEM) != cudaSuccess)
+        return false;
+    for (int S = 1; S <= 8; S *= 2) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)S * 128);
+        cfg.blockDim = dim3(W4_THREADS);
+        cfg.dynamicSmemBytes = W4_SMEM;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = (unsigned)S;
+        at[0].val.clusterDim.y = 1;
+        at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, k, &cfg) != cudaSuccess) return false;
+        d.clusters[S] = std::max(1, n);
+    }
+    if (d.id < 64) known[d.id] = d;
+    return true;
 }
 
 // Cluster size, clusters, and the shared-memory split of one call.
 struct W4Plan {
-    int S, C, tile, NT, phase, batch, slots;
+    int S, C, tile, NT, KB, SG, steps, phase, phases, batch, slots, x_off, xsum_off, part_off, counts_off;
+    bool offs;
     size_t smem;
 };
-W4Plan w4_plan(const W4Layout& L, int64_t tokens, int planes, int sms) {
+W4Plan w4_plan(const W4Layout& L, int format, int64_t tokens, bool x_f32, bool y_f32, const Dev& d) {
     W4Plan best{};
     int64_t best_cost = -1;
+    const int planes = x_f32 ? 3 : 1;
     const int NT = tokens <= 8 ? 1 : tokens <= 16 ? 2 : 4;
     const int tile = (int)std::min<int64_t>(tokens, 8 * NT);
+    const int KB = L.kb, SG = L.sg, fmt = format & (DFLASH2_W4_SCALE_F32 | DFLASH2_W4_ZERO);
+    const int x_off = W4_WARPS * w4_stages(KB, SG, fmt & 2 ? 2 : fmt) * w4_stage_bytes(KB, SG, fmt & 2 ? 2 : fmt);
     const size_t slot = (size_t)NT * 8 * 32 * sizeof(float);
-    for (int S = 1; S <= 8 && S <= L.chunks; S *= 2) {
+    const int steps = L.steps;
+    for (int S = 1; S <= 8 && S <= steps; S *= 2) {
         W4Plan P{};
         P.S = S;
         P.NT = NT;
         P.tile = tile;
-        P.C = (int)std::min<int64_t>(L.units, std::max(1, sms / S));
-        const int kc = (L.chunks + S - 1) / S;  // a CTA's share of K
+        P.KB = KB;
+        P.SG = SG;
+        P.steps = steps;
+        P.offs = !x_f32 && !y_f32;
+        P.C = (int)std::min<int64_t>(L.units, d.clusters[S]);
+        const int kc = (steps + S - 1) / S;  // a CTA's share of K
         const int64_t cu = (L.units + P.C - 1) / P.C;
-        const size_t xc = (size_t)2 * planes * tile * 64;  // bytes of x per chunk
-        // at most this much for x, the rest for the sums
-        P.phase = (int)std::min<int64_t>(kc, (int64_t)(160 * 1024 / xc));
-        const size_t left = W4_SMEM - P.phase * xc;
+        // bytes of a step's x, and of its sums
+        const size_t xb = (size_t)KB * 2 * planes * tile * 64;
+        const size_t xq = P.offs ? (size_t)SG * 8 * NT * sizeof(float) : 0;
+        // at most this much for x, the rest for the sums; phases of one length
+        const int most_x = std::max(1, (int)((W4_SMEM - x_off - W4_WARPS * (slot + 8)) / (xb + xq)));
+        P.phases = (kc + most_x - 1) / most_x;
+        P.phase = (kc + P.phases - 1) / P.phases;
+        P.x_off = x_off;
+        P.xsum_off = x_off + (int)(P.phase * xb);
+        P.part_off = x_off + (int)(P.phase * (xb + xq));
+        const size_t left = W4_SMEM - P.part_off;
         // a unit's items are in ceil((nc - 1) / shortest run) + 1 runs at most
-        for (P.batch = (int)std::min<int64_t>(cu, 1024); P.batch >= 1; --P.batch) {
+        for (P.batch = (int)std::min<int64_t>(cu, left / slot); P.batch >= 1; --P.batch) {
             int most = 1;
-            // the batches of the range: full ones and the last one
+            // the batches of the range: full ones and the last one; the phases
+            // of a longer and of a shorter share of K
             for (int64_t nu : {(int64_t)P.batch, cu % P.batch, (cu - 1) % P.batch}) {
                 if (nu <= 0) continue;
-                for (int nc : {P.phase, kc % P.phase, (L.chunks / S) % P.phase, L.chunks / S}) {
+                for (int nc : {P.phase, kc - (P.phases - 1) * P.phase,
+                               steps / S - (P.phases - 1) * P.phase, steps / S}) {
                     nc = std::min(nc, P.phase);
                     if (nc <= 0) continue;
                     const int64_t run = nu * nc / W4_WARPS;
@@ -489,11 +635,16 @@ W4Plan w4_plan(const W4Layout& L, int64_t tokens, int planes, int sms) {
                 }
             }
             P.slots = most;
-            if ((size_t)P.batch * P.slots * slot <= left) break;
+            if (P.batch * (P.slots * slot + S) <= left) break;
         }
-        P.smem = P.phase * xc + (size_t)P.batch * P.slots * slot;
-        // items a CTA streams, and about a microsecond's worth for the cluster's barriers
-        const int64_t cost = cu * kc + (S > 1 ? 40 : 0);
+        P.counts_off = P.part_off + (int)(P.batch * P.slots * slot);
+        P.smem = P.counts_off + (size_t)P.batch * S;
+        // chunks a CTA streams, and some for the joining of each batch's sums and
+        // for each filling of x (a chunk of a unit takes an SM about 25 ns)
+        const int64_t batches = (cu + P.batch - 1) / P.batch;
+        const int64_t fills = P.phases > 1 ? P.phases * batches : 1;
+        const int64_t cost = cu * kc * KB + batches * (S > 1 ? 40 : 20) +
+                             fills * (40 + (int64_t)P.phase * (int64_t)xb / 4096);
         if (best_cost < 0 || cost < best_cost) {
             best = P;
             best_cost = cost;
@@ -502,9 +653,9 @@ W4Plan w4_plan(const W4Layout& L, int64_t tokens, int planes, int sms) {
     return best;
 }
 
-template <typename XT, int NT, int FMT, bool G32>
+template <typename XT, int NT, int FMT, bool G32, int KB, bool OFFS>
 int launch(const W4Args& a, const W4Plan& P, int dev, cudaStream_t s) {
-    auto* k = linear_w4_kernel<XT, NT, FMT, G32>;
+    auto* k = linear_w4_kernel<XT, NT, FMT, G32, KB, OFFS>;
     {
         static std::mutex mu;
         static bool attr_set[64] = {};
@@ -531,25 +682,30 @@ int launch(const W4Args& a, const W4Plan& P, int dev, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, k, a) == cudaSuccess ? DFLASH2_OK
                                                          : (cudaGetLastError(), DFLASH2_ECUDA);
 }
-template <typename XT, int FMT, bool G32>
+template <typename XT, int FMT, bool G32, int KB, bool OFFS>
 int launch_nt(const W4Args& a, const W4Plan& P, int dev, cudaStream_t s) {
     switch (P.NT) {
-        case 1: return launch<XT, 1, FMT, G32>(a, P, dev, s);
-        case 2: return launch<XT, 2, FMT, G32>(a, P, dev, s);
-        default: return launch<XT, 4, FMT, G32>(a, P, dev, s);
+        case 1: return launch<XT, 1, FMT, G32, KB, OFFS>(a, P, dev, s);
+        case 2: return launch<XT, 2, FMT, G32, KB, OFFS>(a, P, dev, s);
+        default: return launch<XT, 4, FMT, G32, KB, OFFS>(a, P, dev, s);
     }
 }
-template <typename XT>
+template <typename XT, int FMT, bool OFFS>
+int launch_group(const W4Args& a, const W4Plan& P, int dev, cudaStream_t s) {
+    if (P.KB == 2) return launch_nt<XT, FMT, false, 2, OFFS>(a, P, dev, s);
+    return P.SG == 2 ? launch_nt<XT, FMT, true, 1, OFFS>(a, P, dev, s)
+                         : launch_nt<XT, FMT, false, 1, OFFS>(a, P, dev, s);
+}
+template <typename XT, bool OFFS>
 int launch_fmt(const W4Args& a, const W4Plan& P, int format, int dev, cudaStream_t s) {
-    const bool g32 = a.group == 32;
-    if (format & DFLASH2_W4_SCALE_F32)
-        return g32 ? launch_nt<XT, 2, true>(a, P, dev, s)
-                   : launch_nt<XT, 2, false>(a, P, dev, s);
-    if (format & DFLASH2_W4_ZERO)
-        return g32 ? launch_nt<XT, 1, true>(a, P, dev, s)
-                   : launch_nt<XT, 1, false>(a, P, dev, s);
-    return g32 ? launch_nt<XT, 0, true>(a, P, dev, s)
-               : launch_nt<XT, 0, false>(a, P, dev, s);
+    if (format & DFLASH2_W4_SCALE_F32) return launch_group<XT, 2, OFFS>(a, P, dev, s);
+    if (format & DFLASH2_W4_ZERO) return launch_group<XT, 1, OFFS>(a, P, dev, s);
+    return launch_group<XT, 0, OFFS>(a, P, dev, s);
+}
+int launch_any(const W4Args& a, const W4Plan& P, int format, int dtype, int dev, cudaStream_t s) {
+    if (dtype == DFLASH2_F32) return launch_fmt<float, false>(a, P, format, dev, s);
+    return P.offs ? launch_fmt<__nv_bfloat16, true>(a, P, format, dev, s)
+                  : launch_fmt<__nv_bfloat16, false>(a, P, format, dev, s);
 }
 
 constexpr int W4_FORMATS = DFLASH2_W4_ZERO | DFLASH2_W4_SCALE_F32 | DFLASH2_W4_TAPS;
@@ -557,24 +713,22 @@ constexpr int64_t W4_MAX_TOKENS = 1 << 18;
 
 W4Args w4_args(const W4Layout& L, const W4Plan& P, const void* packed) {
     W4Args a{};
-    a.weights = (const uint8_t*)packed;
-    a.scales = (const uint8_t*)packed + L.scale_off;
+    a.packed = (const uint8_t*)packed;
     a.N = L.N;
     a.K = L.K;
     a.units = L.units;
-    a.chunks = L.chunks;
-    a.groups = L.groups;
-    a.group = L.group;
     a.S = P.S;
     a.C = P.C;
+    a.steps = P.steps;
     a.tile = P.tile;
     a.phase = P.phase;
-    a.phases = ((L.chunks + P.S - 1) / P.S + P.phase - 1) / P.phase;
-    a.gdiv = std::max(1, L.group / W4_CHUNK);
-    // ceil(2^32 / gdiv): exact for chunk * gdiv < 2^32, and both are at most 2^14
-    a.gmagic = (uint32_t)(((1ull << 32) + a.gdiv - 1) / a.gdiv);
+    a.phases = P.phases;
     a.batch = P.batch;
     a.slots = P.slots;
+    a.x_off = P.x_off;
+    a.xsum_off = P.xsum_off;
+    a.part_off = P.part_off;
+    a.counts_off = P.counts_off;
     return a;
 }
 
@@ -597,7 +751,7 @@ extern "C" int dflash2_w4_pack(const uint8_t* q, const void* scale, const uint8_
         !aligned(packed, 256))
         return DFLASH2_EALIGN;
     const W4Layout L = w4_layout(N, K, group, format);
-    const int64_t n = L.units * L.chunks * (W4_BLOCK / 16) + L.units * L.groups * W4_UNIT;
+    const int64_t n = L.units * L.steps * (L.kb * (W4_CHUNK_BYTES / 16) + L.sg * W4_UNIT);
     const unsigned blocks = (unsigned)std::min<int64_t>((n + 255) / 256, 148 * 32);
     w4_pack_kernel<<<blocks, 256, 0, (cudaStream_t)stream>>>(q, scale, zero, L, format,
                                                              (uint8_t*)packed);
@@ -619,7 +773,7 @@ extern "C" int dflash2_linear_w4(const void* x, int dtype, int64_t x_stride, int
     Dev d;
     if (!device_info(d)) return DFLASH2_ECUDA;
     const W4Layout L = w4_layout(N, K, group, format);
-    const W4Plan P = w4_plan(L, tokens, dtype == DFLASH2_F32 ? 3 : 1, d.sms);
+    const W4Plan P = w4_plan(L, format, tokens, dtype == DFLASH2_F32, out_dtype == DFLASH2_F32, d);
     W4Args a = w4_args(L, P, packed);
     a.x = x;
     a.x_stride = x_stride;
@@ -628,8 +782,7 @@ extern "C" int dflash2_linear_w4(const void* x, int dtype, int64_t x_stride, int
     a.y = y;
     a.y_bf16 = out_dtype == DFLASH2_BF16;
     cudaStream_t s = (cudaStream_t)stream;
-    return dtype == DFLASH2_BF16 ? launch_fmt<__nv_bfloat16>(a, P, format, d.id, s)
-                                 : launch_fmt<float>(a, P, format, d.id, s);
+    return launch_any(a, P, format, dtype, d.id, s);
 }
 
 extern "C" int dflash2_dynconv2_w4(const void* x, const void* x_prev, const void* packed, int group,
@@ -648,7 +801,7 @@ extern "C" int dflash2_dynconv2_w4(const void* x, const void* x_prev, const void
     if (!device_info(d)) return DFLASH2_ECUDA;
     const int64_t tokens = (int64_t)B * T;
     const W4Layout L = w4_layout(2 * (int64_t)H, H, group, format);
-    const W4Plan P = w4_plan(L, tokens, dtype == DFLASH2_F32 ? 3 : 1, d.sms);
+    const W4Plan P = w4_plan(L, format, tokens, dtype == DFLASH2_F32, dtype == DFLASH2_F32, d);
     W4Args a = w4_args(L, P, packed);
     a.x = x;
     a.x_stride = H;
@@ -660,8 +813,7 @@ extern "C" int dflash2_dynconv2_w4(const void* x, const void* x_prev, const void
     a.y_bf16 = dtype == DFLASH2_BF16;
     cudaStream_t s = (cudaStream_t)stream;
     const int fmt = format & ~DFLASH2_W4_TAPS;
-    return dtype == DFLASH2_BF16 ? launch_fmt<__nv_bfloat16>(a, P, fmt, d.id, s)
-                                 : launch_fmt<float>(a, P, fmt, d.id, s);
+    return launch_any(a, P, fmt, dtype, d.id, s);
 }
 
 unsigned dfl_errors_w4(int clear) {

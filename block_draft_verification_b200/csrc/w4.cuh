@@ -3,30 +3,42 @@
 //
 //   W[n, k] = scale[n, k / group] * (q[n, k] - zero[n, k / group])
 //
-// The packed buffer is [weights][scales].
+// Rows are taken in units of 32, K in chunks of 64, and chunks in steps of two
+// where the group is a multiple of 128 (else one).  The packed buffer is one
+// block per unit and step, at (unit * steps + step) * step_bytes: the step's
+// chunks, 1 KB each, then its scales, so that whatever a run of steps needs is
+// contiguous.
 //
-// Weights: rows in units of 32, K in chunks of 64; unit u, chunk c is the
-// 1 KB block at (u * KC + c) * 1024 (KC chunks per row).  A block holds two
-// 16-row halves of 512 bytes, each the operand of four m16n8k16 products: the
-// 16 bytes of lane l are rows r = l / 4 and r + 8, and of each row the 8 codes
-// at k = 64 c + 32 h + 8 (l mod 4) for h = 0, 1 (words: r h0, r h1, r+8 h0,
-// r+8 h1).  So one 16-byte load per lane, contiguous over the warp, feeds four
-// products, and 8 consecutive k of a row are one word, one 16-byte piece of a
-// K-major bf16 tile.  Within a word, code e sits at nibble e / 2 (e even) or
-// 4 + e / 2 (e odd): (word >> 4 j) & 0x000F000F is the pair (2 j, 2 j + 1).
+// A chunk holds two 16-row halves of 512 bytes, each the operand of four
+// m16n8k16 products: the 16 bytes of lane l are rows r = l / 4 and r + 8, and of
+// each row the 8 codes at k = 64 c + 32 h + 8 (l mod 4) for h = 0, 1 (words:
+// r h0, r h1, r+8 h0, r+8 h1).  So one 16-byte load per lane, contiguous over the
+// warp, feeds four products, and 8 consecutive k of a row are one word, one
+// 16-byte piece of a
+// K-major bf16 tile.  A word is eight nibbles turned left by three bits; code
+// e is nibble e / 2 (e even) or 4 + e / 2 (e odd), so turning the word right by
+// 4 j leaves the pair (2 j, 2 j + 1) in bits 3..6 of its two halves, the top of
+// a bf16 mantissa (j = 0 needs no turn).
 //
-// Scales: per unit and group of K, the 32 rows' entries in the order
-// (r mod 8, r / 8), so the four rows a lane works on are adjacent:
+// Scales: per group of the step (two where the group is 32), the 32 rows'
+// entries in the order (r mod 8, r / 8), so the four rows a lane works on are
+// adjacent:
 //   format 0 (bf16 scales, zero = 8): 4 bf16 per lane-row, 64 bytes a group
 //   DFLASH2_W4_ZERO:                  4 bf16 + 4 bf16 of (128 + zero), 128 bytes
 //   DFLASH2_W4_SCALE_F32:             4 float + 4 bf16 of (128 + zero) + 8 pad, 256 bytes
 // Rows past N have scale 0; the K tail of a last half chunk has codes equal
 // to its zero point and, where it is a group of its own, scale 0.
 //
-// Codes to operands: 0x4300 | q is the bf16 value 128 + q; subtracting
-// (128 + zero) leaves q - zero, an integer of at most 8 bits, exactly.  The
-// products with x then accumulate in fp32 with no rounding of the weights, and
-// the group's scale multiplies the fp32 sum.
+// Codes to operands, two ways:
+//   - exact: 0x4300 | q is the bf16 value 128 + q; subtracting (128 + zero)
+//     leaves q - zero, an integer of at most 8 bits, exactly.  The products with
+//     x then accumulate in fp32 with no rounding of the weights, and the group's
+//     scale multiplies the fp32 sum.
+//   - offset: 0x4180 | q << 3 is 16 + q, with no subtraction, and the sum starts
+//     at -(16 + zero) * sum of x instead of zero.  A third fewer instructions,
+//     but the fp32 sum passes through magnitudes a few times those of the
+//     result, and its last bits go with them (about 2e-6 of the result): it
+//     serves bf16 outputs, whose own rounding is a thousand times that.
 #pragma once
 
 #include "common.cuh"
@@ -35,7 +47,7 @@ namespace dfl {
 
 constexpr int W4_UNIT = 32;         // rows per unit
 constexpr int W4_CHUNK = 64;        // K per chunk
-constexpr int W4_BLOCK = 1024;      // bytes per unit and chunk
+constexpr int W4_CHUNK_BYTES = 1024;  // of one unit
 
 // Bytes of one unit's scales for one group of K, by format.
 __host__ __device__ constexpr int w4_scale_bytes(int format) {
@@ -46,10 +58,10 @@ struct W4Layout {
     int64_t N, K;
     int64_t units;    // of 32 rows
     int chunks;       // of 64 k, the last one possibly half
-    int groups;       // per row as packed: K / group, or 2 per chunk for group 32
+    int kb, sg;       // chunks and groups (1, or 2 of 32) of a step
+    int steps;        // chunks / kb
     int group;
-    int sbytes;       // scale bytes per unit and group
-    size_t scale_off; // bytes
+    int step_bytes;
     size_t total;
 };
 
@@ -65,25 +77,35 @@ __host__ __device__ inline W4Layout w4_layout(int64_t N, int64_t K, int group, i
     L.K = K;
     L.units = (N + W4_UNIT - 1) / W4_UNIT;
     L.chunks = (int)((K + W4_CHUNK - 1) / W4_CHUNK);
+    L.kb = group % 128 == 0 ? 2 : 1;
+    L.sg = group == 32 ? 2 : 1;
+    L.steps = L.chunks / L.kb;
     L.group = group;
-    L.groups = group == 32 ? 2 * L.chunks : (int)(K / group);
-    L.sbytes = w4_scale_bytes(format);
-    L.scale_off = (size_t)L.units * L.chunks * W4_BLOCK;
-    L.total = L.scale_off + (size_t)L.units * L.groups * L.sbytes;
+    L.step_bytes = L.kb * W4_CHUNK_BYTES + L.sg * w4_scale_bytes(format);
+    L.total = (size_t)L.units * L.steps * L.step_bytes;
     return L;
 }
 
-// The pair (2 j, 2 j + 1) of a word, minus the zero points, as bf16x2.
-// zz = bf16x2 of (128 + zero) twice.
-__device__ __forceinline__ uint32_t w4_pair(uint32_t w, int j, uint32_t zz) {
+__device__ __forceinline__ uint32_t w4_turn(uint32_t w, int bits) {
+    return bits == 0 ? w : __funnelshift_r(w, w, bits);
+}
+// (w & mask) | magic in one three-input operation
+__device__ __forceinline__ uint32_t w4_and_or(uint32_t w, uint32_t mask, uint32_t magic) {
     uint32_t t;
-    // (w >> 4 j & 0x000F000F) | 0x43004300 in one three-input operation
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;"
-        : "=r"(t)
-        : "r"(w >> (4 * j)), "r"(0x000F000Fu), "r"(0x43004300u));
-    __nv_bfloat162 d = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&t),
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(t) : "r"(w), "r"(mask), "r"(magic));
+    return t;
+}
+// The pair (2 j, 2 j + 1) of a word as bf16x2, minus the zero points; zz =
+// bf16x2 of (128 + zero) twice.
+__device__ __forceinline__ uint32_t w4_pair_exact(uint32_t w, int j, uint32_t zz) {
+    const uint32_t t = w4_and_or(w4_turn(w, 3 + 4 * j), 0x000F000Fu, 0x43004300u);
+    __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&t),
                                *reinterpret_cast<const __nv_bfloat162*>(&zz));
     return *reinterpret_cast<uint32_t*>(&d);
+}
+// The same plus 16, zero points left in.
+__device__ __forceinline__ uint32_t w4_pair_offset(uint32_t w, int j) {
+    return w4_and_or(w4_turn(w, 4 * j), 0x00780078u, 0x41804180u);
 }
 
 // The scales (and zero points) of the four rows r, r + 8, r + 16, r + 24 of a
@@ -91,17 +113,18 @@ __device__ __forceinline__ uint32_t w4_pair(uint32_t w, int j, uint32_t zz) {
 template <int FMT>
 struct W4Scale {
     uint32_t raw[(FMT & DFLASH2_W4_SCALE_F32) ? 6 : (FMT & DFLASH2_W4_ZERO) ? 4 : 2];
-    // p: the group's entries of this unit; g = r mod 8
-    __device__ __forceinline__ void load(const uint8_t* p, int g) {
+    static constexpr int BYTES = w4_scale_bytes(FMT) / 8;
+    // p: the entries of this lane's four rows
+    __device__ __forceinline__ void load(const uint8_t* p) {
         if constexpr ((FMT & DFLASH2_W4_SCALE_F32) != 0) {
-            const uint4 a = __ldg((const uint4*)(p + 32 * g));
-            const uint2 b = __ldg((const uint2*)(p + 32 * g + 16));
+            const uint4 a = *(const uint4*)p;
+            const uint2 b = *(const uint2*)(p + 16);
             raw[0] = a.x, raw[1] = a.y, raw[2] = a.z, raw[3] = a.w, raw[4] = b.x, raw[5] = b.y;
         } else if constexpr ((FMT & DFLASH2_W4_ZERO) != 0) {
-            const uint4 a = __ldg((const uint4*)(p + 16 * g));
+            const uint4 a = *(const uint4*)p;
             raw[0] = a.x, raw[1] = a.y, raw[2] = a.z, raw[3] = a.w;
         } else {
-            const uint2 a = __ldg((const uint2*)(p + 8 * g));
+            const uint2 a = *(const uint2*)p;
             raw[0] = a.x, raw[1] = a.y;
         }
     }
@@ -114,6 +137,12 @@ struct W4Scale {
         if constexpr (FMT == 0) return 0x43084308u;  // 128 + 8
         const uint32_t w = raw[((FMT & DFLASH2_W4_SCALE_F32) ? 4 : 2) + (i >> 1)];
         return (i & 1) ? __byte_perm(w, 0, 0x3232) : __byte_perm(w, 0, 0x1010);
+    }
+    // 16 + zero
+    __device__ __forceinline__ float zero16(int i) const {
+        if constexpr (FMT == 0) return 24.0f;
+        const uint32_t w = raw[((FMT & DFLASH2_W4_SCALE_F32) ? 4 : 2) + (i >> 1)];
+        return __uint_as_float((i & 1) ? (w & 0xFFFF0000u) : (w << 16)) - 112.0f;
     }
 };
 
