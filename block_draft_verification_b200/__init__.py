@@ -14,6 +14,7 @@ import torch
 __all__ = ["F32", "BF16", "Q_SOFTMAX", "Q_ONEHOT", "K", "DFlash2Error", "lib", "workspace_bytes",
            "Workspace", "topk_softmax", "pair_select", "verify_greedy", "verify_sample",
            "verify_sample_trunc", "dynconv2", "PackedTap", "PackedW4", "linear_w4",
+           "norm_residual", "GATE_LINEAR", "GATE_SIGMOID",
            "status_string", "version", "device_errors"]
 
 F32, BF16 = 0, 1
@@ -73,6 +74,8 @@ def lib():
         L.dflash2_w4_pack.argtypes = [vp, vp, vp, i64, i64, i32, i32, vp, vp]
         L.dflash2_linear_w4.argtypes = [vp, i32, i64, i64, vp, i64, i64, i32, i32, vp, i32, vp]
         L.dflash2_dynconv2_w4.argtypes = [vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp]
+        L.dflash2_norm_residual.argtypes = [vp, i32, i64, vp, i32, i64, vp, i64, i64, i32, vp, vp,
+                                            f32, f32, f32, i64, i64, vp, vp, vp]
         L.dflash2_device_errors.argtypes = [i32]
         L.dflash2_device_errors.restype = C.c_uint32
         for f in ("dflash2_topk_softmax", "dflash2_topk_softmax_ex", "dflash2_pair_select",
@@ -80,7 +83,7 @@ def lib():
                   "dflash2_verify_greedy", "dflash2_verify_sample", "dflash2_verify_sample_ex",
                   "dflash2_verify_sample_trunc", "dflash2_dynconv2", "dflash2_dynconv2_pack",
                   "dflash2_dynconv2_packed", "dflash2_w4_pack", "dflash2_linear_w4",
-                  "dflash2_dynconv2_w4"):
+                  "dflash2_dynconv2_w4", "dflash2_norm_residual"):
             getattr(L, f).restype = i32
         _lib = L
     return _lib
@@ -479,3 +482,68 @@ def _dynconv2_w4(x, x_prev, w4, out):
     _call("dflash2_dynconv2_w4", x.device, x.data_ptr(), x_prev.data_ptr(), w4.buf.data_ptr(),
           w4.group, w4.format, _dtype(x), B, T, H, out.data_ptr())
     return out
+
+
+GATE_LINEAR, GATE_SIGMOID = 0, 1
+
+
+def _rows(t, H):
+    """t [..., H] as (tensor, row stride) of one run of rows."""
+    t2 = t if t.dim() == 2 else t.reshape(-1, H)
+    if t2.stride(1) != 1 or (t2.shape[0] > 1 and t2.stride(0) < H):
+        t2 = t2.contiguous()
+    return t2, max(t2.stride(0), H)
+
+
+def norm_residual(res, y, w_post=None, w_pre=None, gate=None, gate_act=GATE_LINEAR, scale=1.0,
+                  eps=1e-6, w_offset=0.0, out=None):
+    """The norms around a block (dflash2_norm_residual):
+    r' = res + scale * act(gate) * rms(y; w_post), h = rms(r'; w_pre).
+    res, y [..., H] (y float32 or bfloat16, res of y's type or float32; rows may
+    be strided); gate [H] (per channel), [B, H] with y [B, T, H] (per sequence) or
+    y's shape (per token), or None; w_post, w_pre [H] or None; gate and weights of
+    y's type.  Returns (r', h), or r' alone without w_pre.  out: (r', h) or r' to
+    write to; r' may be res."""
+    H = y.shape[-1]
+    dev, dt = y.device, y.dtype
+    _cuda(res, y, gate, w_post, w_pre)
+    _same_device(dev, res, gate, w_post, w_pre)
+    if res.shape != y.shape:
+        raise ValueError("res and y have one shape")
+    for t in (gate, w_post, w_pre):
+        if t is not None and t.dtype != dt:
+            raise TypeError("the gate and the weights have y's type")
+    for w in (w_post, w_pre):
+        if w is not None and w.shape != (H,):
+            raise ValueError("norm weights are [H]")
+    y2, ys = _rows(y, H)
+    r2, rs = _rows(res, H)
+    rows = y2.shape[0]
+    gp, gs, rep = None, H, 1
+    if gate is not None:
+        if gate.shape == (H,):
+            rep, g2 = max(rows, 1), gate.contiguous()
+        elif gate.shape == y.shape:
+            g2, gs = _rows(gate, H)
+        elif y.dim() == 3 and gate.shape == (y.shape[0], H):
+            rep = max(y.shape[1], 1)
+            g2, gs = _rows(gate, H)
+        else:
+            raise ValueError("gate is [H], [B, H] or like y")
+        gp = g2.data_ptr()
+    w_post = None if w_post is None else w_post.contiguous()
+    w_pre = None if w_pre is None else w_pre.contiguous()
+    if out is None:
+        r_out = torch.empty(y.shape, dtype=res.dtype, device=dev)
+        h = torch.empty(y.shape, dtype=dt, device=dev) if w_pre is not None else None
+    else:
+        r_out, h = out if w_pre is not None else (out, None)
+        for t, like in ((r_out, res), (h, y)):
+            if t is not None and (t.shape != y.shape or t.dtype != like.dtype or
+                                  not t.is_contiguous() or t.device != dev):
+                raise ValueError("out is not a dense tensor like res (and y)")
+    _call("dflash2_norm_residual", dev, r2.data_ptr(), _dtype(res), rs, y2.data_ptr(), _dtype(y), ys,
+          gp, gs, rep, gate_act, None if w_post is None else w_post.data_ptr(),
+          None if w_pre is None else w_pre.data_ptr(), w_offset, scale, eps, rows, H,
+          r_out.data_ptr(), None if h is None else h.data_ptr())
+    return r_out if h is None else (r_out, h)

@@ -1,0 +1,270 @@
+// norm_residual.cu -- the norms around a block, fused with the block's gate and
+// residual scale:
+//
+//   r' = r + alpha * act(g) * rms(y; w_post),   h = rms(r'; w_pre),
+//   rms(v; w)_i = v_i / sqrt(mean_j v_j^2 + eps) * (w_i + w_offset)
+//
+// One pass over memory: a row's y and r are read once, kept in registers while
+// the sum of squares of y, then of r', is formed in fp32, and r' and h are
+// written once.  h is taken from r' before its rounding.  A row is worked on
+// by a group of threads sized to it, so that few rows still spread over the
+// device and many rows keep all of it streaming; rows too long for registers
+// are read again from cache (three passes).
+#include <algorithm>
+
+#include "common.cuh"
+
+namespace dfl {
+
+struct NormArgs {
+    const void* res;
+    const void* y;
+    const void* gate;    // NULL: none
+    const void* w_post;  // NULL: y is taken as it is
+    const void* w_pre;   // NULL: no second norm, h is not written
+    void* res_out;
+    void* h;
+    int64_t rows, H, res_stride, y_stride, gate_stride, gate_rep;
+    float alpha, eps, w_offset;
+    int sigmoid;
+};
+
+// N consecutive elements widened to fp32 (vec: one 16-byte load, or two).
+template <typename T, int N>
+__device__ __forceinline__ void ld_n(const T* p, float (&v)[N]) {
+    if constexpr (sizeof(T) == 2) {
+        static_assert(N == 8, "bf16 vectors are 8 wide");
+        const uint4 q = *(const uint4*)p;
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            const float4 q = *(const float4*)(p + 4 * i);
+            v[4 * i] = q.x, v[4 * i + 1] = q.y, v[4 * i + 2] = q.z, v[4 * i + 3] = q.w;
+        }
+    }
+}
+template <typename T, int N>
+__device__ __forceinline__ void st_n(T* p, const float (&v)[N]) {
+    if constexpr (sizeof(T) == 2) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        *(uint4*)p = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i)
+            *(float4*)(p + 4 * i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    }
+}
+__device__ __forceinline__ float ld_1(const float* p) { return *p; }
+__device__ __forceinline__ float ld_1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ void st_1(float* p, float v) { *p = v; }
+__device__ __forceinline__ void st_1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+__device__ __forceinline__ float act(float g, int sigmoid) {
+    return sigmoid ? 1.0f / (1.0f + expf(-g)) : g;
+}
+
+// Sum over the block, the same value in every thread (`buf`: 32 floats, free
+// for the next call one barrier later).
+__device__ __forceinline__ float block_sum(float v, float* buf) {
+#pragma unroll
+    for (int j = 16; j > 0; j >>= 1) v += __shfl_xor_sync(FULL, v, j);
+    const int nw = blockDim.x >> 5;
+    if (nw == 1) return v;
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = (threadIdx.x & 31) < nw ? buf[threadIdx.x & 31] : 0.0f;
+#pragma unroll
+    for (int j = 16; j > 0; j >>= 1) v += __shfl_xor_sync(FULL, v, j);
+    return v;
+}
+
+// XT: y, gate, weights and h; RT: the residual.  V vectors of 8 per thread held
+// in registers (H <= 8 V blockDim, H a multiple of 8, 16-byte rows).
+template <typename XT, typename RT, int V>
+__global__ void __launch_bounds__(512) norm_residual_kernel(const NormArgs a) {
+    __shared__ float buf[2][32];
+    const int n8 = (int)(a.H / 8);
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const XT* y = (const XT*)a.y + row * a.y_stride;
+        const RT* r = (const RT*)a.res + row * a.res_stride;
+        const XT* g = a.gate ? (const XT*)a.gate + row / a.gate_rep * a.gate_stride : nullptr;
+        float vy[V][8], vr[V][8];
+        float ss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int q = threadIdx.x + i * blockDim.x;
+            if (q < n8) {
+                ld_n<XT, 8>(y + 8 * q, vy[i]);
+                ld_n<RT, 8>(r + 8 * q, vr[i]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ss = fmaf(vy[i][e], vy[i][e], ss);
+            }
+        }
+        float inv = a.alpha;
+        if (a.w_post) inv *= rsqrtf(block_sum(ss, buf[0]) / (float)a.H + a.eps);
+        float s2 = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int q = threadIdx.x + i * blockDim.x;
+            if (q < n8) {
+                float f[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = inv;
+                if (a.w_post) {
+                    float w[8];
+                    ld_n<XT, 8>((const XT*)a.w_post + 8 * q, w);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) f[e] *= w[e] + a.w_offset;
+                }
+                if (g) {
+                    float w[8];
+                    ld_n<XT, 8>(g + 8 * q, w);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) f[e] *= act(w[e], a.sigmoid);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    vr[i][e] = fmaf(f[e], vy[i][e], vr[i][e]);
+                    s2 = fmaf(vr[i][e], vr[i][e], s2);
+                }
+                st_n<RT, 8>((RT*)a.res_out + row * a.H + 8 * q, vr[i]);
+            }
+        }
+        if (a.w_pre) {
+            const float inv2 = rsqrtf(block_sum(s2, buf[1]) / (float)a.H + a.eps);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int q = threadIdx.x + i * blockDim.x;
+                if (q < n8) {
+                    float w[8];
+                    ld_n<XT, 8>((const XT*)a.w_pre + 8 * q, w);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) w[e] = vr[i][e] * inv2 * (w[e] + a.w_offset);
+                    st_n<XT, 8>((XT*)a.h + row * a.H + 8 * q, w);
+                }
+            }
+        }
+        if (gridDim.x < a.rows) __syncthreads();  // the sums' buffers are used again
+    }
+}
+
+// Any width, stride and alignment: element by element, y and r read again from
+// cache after each sum.  r' is recomputed in the last pass, not read back, so
+// that h comes from the unrounded value; where the output is written over the
+// residual, r' of a row is written only after its last read.
+template <typename XT, typename RT>
+__global__ void __launch_bounds__(512) norm_residual_any_kernel(const NormArgs a) {
+    __shared__ float buf[2][32];
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const XT* y = (const XT*)a.y + row * a.y_stride;
+        const RT* r = (const RT*)a.res + row * a.res_stride;
+        const XT* g = a.gate ? (const XT*)a.gate + row / a.gate_rep * a.gate_stride : nullptr;
+        const XT* wpost = (const XT*)a.w_post;
+        const XT* wpre = (const XT*)a.w_pre;
+        float inv = a.alpha;
+        if (wpost) {
+            float ss = 0.0f;
+            for (int64_t i = threadIdx.x; i < a.H; i += blockDim.x) {
+                const float v = ld_1(y + i);
+                ss = fmaf(v, v, ss);
+            }
+            inv *= rsqrtf(block_sum(ss, buf[0]) / (float)a.H + a.eps);
+        }
+        auto sum_at = [&](int64_t i) {
+            float f = inv;
+            if (wpost) f *= ld_1(wpost + i) + a.w_offset;
+            if (g) f *= act(ld_1(g + i), a.sigmoid);
+            return fmaf(f, ld_1(y + i), ld_1(r + i));
+        };
+        float inv2 = 0.0f;
+        if (wpre) {
+            float s2 = 0.0f;
+            for (int64_t i = threadIdx.x; i < a.H; i += blockDim.x) {
+                const float v = sum_at(i);
+                s2 = fmaf(v, v, s2);
+            }
+            inv2 = rsqrtf(block_sum(s2, buf[1]) / (float)a.H + a.eps);
+        }
+        for (int64_t i = threadIdx.x; i < a.H; i += blockDim.x) {
+            const float v = sum_at(i);
+            st_1((RT*)a.res_out + row * a.H + i, v);
+            if (wpre) st_1((XT*)a.h + row * a.H + i, v * inv2 * (ld_1(wpre + i) + a.w_offset));
+        }
+        if (gridDim.x < a.rows) __syncthreads();
+    }
+}
+
+}  // namespace dfl
+
+using namespace dfl;
+using namespace dfl_host;
+
+namespace {
+
+template <typename XT, typename RT>
+int launch(const NormArgs& a, bool vec, cudaStream_t s) {
+    const unsigned grid = (unsigned)std::min<int64_t>(a.rows, 1 << 30);
+    const int64_t n8 = a.H / 8;
+    if (vec && n8 <= 4 * 512) {
+        // a vector or two per thread: the loads of a row are all in flight at once
+        const int threads = (int)std::min<int64_t>(512, std::max<int64_t>(32, (n8 + 31) / 32 * 32));
+        const int v = (int)((n8 + threads - 1) / threads);
+        if (v <= 1)
+            norm_residual_kernel<XT, RT, 1><<<grid, threads, 0, s>>>(a);
+        else if (v <= 2)
+            norm_residual_kernel<XT, RT, 2><<<grid, threads, 0, s>>>(a);
+        else
+            norm_residual_kernel<XT, RT, 4><<<grid, threads, 0, s>>>(a);
+    } else {
+        const int threads = (int)std::min<int64_t>(512, (a.H + 31) / 32 * 32);
+        norm_residual_any_kernel<XT, RT><<<grid, threads, 0, s>>>(a);
+    }
+    return launch_status();
+}
+
+}  // namespace
+
+extern "C" int dflash2_norm_residual(const void* res, int res_dtype, int64_t res_stride,
+                                     const void* y, int dtype, int64_t y_stride, const void* gate,
+                                     int64_t gate_stride, int64_t gate_rep, int gate_act,
+                                     const void* w_post, const void* w_pre, float w_offset,
+                                     float alpha, float eps, int64_t rows, int64_t H,
+                                     void* res_out, void* h, dflash2_stream_t stream) {
+    if (!dtype_ok(dtype) || !dtype_ok(res_dtype)) return DFLASH2_EDTYPE;
+    if (dtype == DFLASH2_F32 && res_dtype == DFLASH2_BF16) return DFLASH2_EDTYPE;
+    if (rows < 0 || rows > (1 << 30) || H < 1 || H > (1 << 24) || res_stride < H || y_stride < H)
+        return DFLASH2_ESHAPE;
+    if (gate && (gate_rep < 1 || (gate_stride < H && gate_rep < rows))) return DFLASH2_ESHAPE;
+    if (!isfinite(alpha) || !isfinite(w_offset) || !isfinite(eps) || eps < 0.0f) return DFLASH2_EINVAL;
+    if (gate_act != DFLASH2_GATE_LINEAR && gate_act != DFLASH2_GATE_SIGMOID) return DFLASH2_EINVAL;
+    if (rows == 0) return DFLASH2_OK;
+    if (!res || !y || !res_out || (w_pre != nullptr) != (h != nullptr)) return DFLASH2_EINVAL;
+    const size_t es = (size_t)elem_size(dtype), rs = (size_t)elem_size(res_dtype);
+    if (!aligned(res, rs) || !aligned(y, es) || !aligned(gate, es) || !aligned(w_post, es) ||
+        !aligned(w_pre, es) || !aligned(res_out, rs) || !aligned(h, es))
+        return DFLASH2_EALIGN;
+    if (res_out == res && res_stride != H && rows > 1) return DFLASH2_EINVAL;  // rows would overlap
+    // 16-byte loads where every row of every operand starts on 16 bytes
+    const bool vec = H % 8 == 0 && aligned(res, 16) && aligned(y, 16) && aligned(gate, 16) &&
+                     aligned(w_post, 16) && aligned(w_pre, 16) && aligned(res_out, 16) &&
+                     aligned(h, 16) &&
+                     (rows == 1 || (res_stride * rs % 16 == 0 && y_stride * es % 16 == 0)) &&
+                     (!gate || gate_rep >= rows || gate_stride * es % 16 == 0);
+    NormArgs a{res, y, gate, w_post, w_pre, res_out, h, rows, H, res_stride, y_stride, gate_stride,
+               gate ? gate_rep : 1, alpha, eps, w_offset, gate_act == DFLASH2_GATE_SIGMOID};
+    cudaStream_t s = (cudaStream_t)stream;
+    if (dtype == DFLASH2_F32) return launch<float, float>(a, vec, s);
+    return res_dtype == DFLASH2_F32 ? launch<__nv_bfloat16, float>(a, vec, s)
+                                    : launch<__nv_bfloat16, __nv_bfloat16>(a, vec, s);
+}

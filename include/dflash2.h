@@ -18,6 +18,8 @@
  *   dflash2_linear_w4      product with weights held in 4 bits with group
  *                          scales (the drafter's projections and its head)
  *   dflash2_dynconv2_w4    the conv with its tap weights held the same way
+ *   dflash2_norm_residual  the norms before and after a block, fused with its
+ *                          gate and residual scale
  *
  * Source pages (cited by title and section):
  *   [tamsi]    "DFlash 2 — 3× plus de tokens sur Qwen3.8-27B, même sortie",
@@ -491,6 +493,46 @@ DFLASH2_API int dflash2_linear_w4(const void* x, int dtype, int64_t x_stride, in
 DFLASH2_API int dflash2_dynconv2_w4(const void* x, const void* x_prev, const void* packed,
                                     int group, int format, int dtype, int B, int T, int H,
                                     void* out, dflash2_stream_t stream);
+
+/*
+ * The norms around a block, fused with the block's gate and residual scale
+ * ([tamsi] "L’idée, sans le papier": the convs sit before and after each
+ * attention and MLP of the drafter, next to its norms).  For every row:
+ *
+ *   r' = res + alpha * act(gate) * rms(y; w_post),   h = rms(r'; w_pre),
+ *   rms(v; w)_i = v_i / sqrt(mean_j v_j^2 + eps) * (w_i + w_offset)
+ *
+ * y is the block's output, r' the residual stream after it, h the input of the
+ * next block.  Sums and products are fp32; h is taken from r' before r' is
+ * rounded; one rounding at each output.
+ *
+ * res         [rows, res_stride] of `res_dtype`: the type of y, or float beside
+ *             bf16 (other pairs: DFLASH2_EDTYPE).
+ * y           [rows, y_stride] of `dtype`;  strides in elements, >= H.
+ * gate        of `dtype`, or NULL for none; row r takes gate row r / gate_rep,
+ *             gate_stride elements apart: gate_rep = 1 for a gate per token, the
+ *             tokens of a sequence for one per sequence, rows (or more) for one
+ *             per channel.
+ * gate_act    DFLASH2_GATE_LINEAR (as it is) or DFLASH2_GATE_SIGMOID.
+ * w_post      [H] of `dtype`, or NULL: y is not normalised.
+ * w_pre       [H] of `dtype`, or NULL with h NULL: no second norm.
+ * rows        in [0, 2^30] (0 is a no-op);  H in [1, 2^24].
+ * alpha, w_offset finite; eps finite, >= 0.
+ * res_out     [rows, H] of `res_dtype`, dense; may be res itself where res is
+ *             dense too (any other overlap is not allowed).
+ * h           [rows, H] of `dtype`, dense.
+ * H a multiple of 8, at most 16,384, with rows that start on 16 bytes is read
+ * with 128-bit loads in one pass; other shapes element by element.  No
+ * workspace.  A row's bits do not depend on the other rows.
+ */
+#define DFLASH2_GATE_LINEAR 0
+#define DFLASH2_GATE_SIGMOID 1
+DFLASH2_API int dflash2_norm_residual(const void* res, int res_dtype, int64_t res_stride,
+                                      const void* y, int dtype, int64_t y_stride, const void* gate,
+                                      int64_t gate_stride, int64_t gate_rep, int gate_act,
+                                      const void* w_post, const void* w_pre, float w_offset,
+                                      float alpha, float eps, int64_t rows, int64_t H,
+                                      void* res_out, void* h, dflash2_stream_t stream);
 
 /*
  * Device-side error flags of the kernels on the current device (0 = none).

@@ -58,6 +58,8 @@ def _sig():
     L.orc_verify_sample_trunc.argtypes = [vp, vp, i32, i32, i32, i64, vp, dbl, i32, dbl, u64,
                                           u32, vp, i32, vp, vp, vp, vp, vp, vp, vp]
     L.orc_dynconv2.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp]
+    L.orc_norm_residual.argtypes = [vp, i32, vp, i32, vp, i64, i32, vp, vp, dbl, dbl, dbl, i64, i64,
+                                    vp, vp]
     L.orc_linear_w4.argtypes = [vp, i32, i64, vp, vp, i32, vp, i64, i64, i64, vp, vp]
 
 
@@ -297,3 +299,18 @@ def dynconv2_w4(x, x_prev, q, scale, zero=None):
     prev = np.concatenate([f64(x_prev)[:, None], cur[:, :-1]], axis=1)
     return (cur + y[:, :, 0] * cur + y[:, :, 1] * prev,
             np.abs(cur) + mag[:, :, 0] * np.abs(cur) + mag[:, :, 1] * np.abs(prev))
+
+
+# ---------------------------------------------------------------- norms around a block
+def norm_residual(res, y, w_post=None, w_pre=None, gate=None, gate_rep=1, sigmoid=False, scale=1.0,
+                  eps=1e-6, w_offset=0.0):
+    """res, y [rows, H], gate [rows of gate, H] -> r' [rows, H] f64, h [rows, H] f64 or None."""
+    r, yy = np.ascontiguousarray(res), np.ascontiguousarray(y)
+    g, wo, wi = (None if t is None else np.ascontiguousarray(t) for t in (gate, w_post, w_pre))
+    rows, H = yy.shape
+    out = np.zeros((rows, H), np.float64)
+    h = None if wi is None else np.zeros((rows, H), np.float64)
+    _check(lib().orc_norm_residual(_p(r), _dtype_of(r), _p(yy), _dtype_of(yy), _p(g), int(gate_rep),
+                                   int(sigmoid), _p(wo), _p(wi), float(w_offset), float(scale),
+                                   float(eps), rows, H, _p(out), _p(h)), "norm_residual")
+    return out, h

@@ -116,6 +116,12 @@ int orc_linear_w4(const void* x, int dtype, int64_t tokens, const uint8_t* q, co
                   int scale_dtype, const uint8_t* zero, int64_t N, int64_t K, int64_t group,
                   double* y, double* abs_sum);
 
+/* ---- the norms around a block with its gate and residual scale ---- */
+int orc_norm_residual(const void* res, int res_dtype, const void* y, int dtype, const void* gate,
+                      int64_t gate_rep, int sigmoid, const void* w_post, const void* w_pre,
+                      double w_offset, double alpha, double eps, int64_t rows, int64_t H,
+                      double* res_out, double* h);
+
 #ifdef __cplusplus
 }
 #endif
