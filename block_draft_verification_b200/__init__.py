@@ -384,12 +384,16 @@ def _dynconv2_packed(x, x_prev, pk, out, ws):
 W4_ZERO, W4_SCALE_F32, W4_TAPS = 1, 2, 4
 
 
-def _call(name, dev, *args):
-    """One library call on the current stream of `dev`, with `dev` current: the
-    library launches on the calling thread's device."""
-    index = dev.index
-    stream = torch._C._cuda_getCurrentRawStream(index)  # current_stream(dev).cuda_stream, without its object
-    f = getattr(_lib or lib(), name)
+_fns = {}
+
+
+def _call(name, index, *args):
+    """One library call on the current stream of device `index`, with that device
+    current: the library launches on the calling thread's device."""
+    f = _fns.get(name)
+    if f is None:
+        f = _fns[name] = getattr(lib(), name)
+    stream = torch._C._cuda_getCurrentRawStream(index)  # current_stream(index).cuda_stream, without its object
     if torch._C._cuda_getDevice() == index:
         rc = f(*args, stream)
     else:
@@ -399,10 +403,11 @@ def _call(name, dev, *args):
         raise DFlash2Error(name, rc)
 
 
-def _same_device(dev, *ts):
-    for t in ts:
-        if t is not None and t.device != dev:
-            raise ValueError("dflash2 calls take tensors of one CUDA device")
+def _like(t, dtype, index):
+    if t.get_device() != index:
+        raise ValueError("dflash2 calls take tensors of one CUDA device")
+    if t.dtype != dtype:
+        raise TypeError("expected %s, got %s" % (dtype, t.dtype))
 
 
 class PackedW4:
@@ -415,7 +420,9 @@ class PackedW4:
 
     def __init__(self, q, scale, zero=None, taps=False):
         _cuda(q, scale, zero)
-        _same_device(q.device, scale, zero)
+        for t in (scale, zero):
+            if t is not None and t.device != q.device:
+                raise ValueError("dflash2 calls take tensors of one CUDA device")
         if q.dtype != torch.uint8 or (zero is not None and zero.dtype != torch.uint8):
             raise TypeError("4-bit codes and zero points are uint8")
         if q.dim() != 2 or scale.dim() != 2 or scale.shape[0] != q.shape[0] or \
@@ -429,14 +436,15 @@ class PackedW4:
         self.format = ((W4_ZERO if zero is not None else 0) |
                        (W4_SCALE_F32 if _dtype(scale) == F32 else 0) | (W4_TAPS if taps else 0))
         self.taps = bool(taps)
-        self.device = q.device
+        self.index = q.get_device()
         n = int(lib().dflash2_w4_packed_bytes(self.N, self.K, self.group, self.format))
         self.buf = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
         q, scale = q.contiguous(), scale.contiguous()
         zero = None if zero is None else zero.contiguous()
-        _call("dflash2_w4_pack", q.device, q.data_ptr(), scale.data_ptr(),
+        _call("dflash2_w4_pack", self.index, q.data_ptr(), scale.data_ptr(),
               None if zero is None else zero.data_ptr(), self.N, self.K, self.group, self.format,
               self.buf.data_ptr())
+        self.ptr = self.buf.data_ptr()
 
 
 def linear_w4(x, w4, out_dtype=None, out=None):
@@ -444,31 +452,31 @@ def linear_w4(x, w4, out_dtype=None, out=None):
     y [..., N] of out_dtype (default x's): y = x W^T (dflash2_linear_w4)."""
     if w4.taps:
         raise ValueError("weights packed as taps are for dynconv2")
-    K, N = w4.K, w4.N
+    K, N, index = w4.K, w4.N, w4.index
     shape = x.shape
     if shape[-1] != K:
         raise ValueError("x has %d columns, the weights K = %d" % (shape[-1], K))
-    if not x.is_cuda or x.device != w4.device:
+    if x.get_device() != index:
         raise ValueError("x and the weights are on one CUDA device")
-    x2 = x if x.dim() == 2 else x.reshape(-1, K)
-    rows, stride = x2.shape[0], x2.stride(0)
-    if x2.stride(1) != 1 or (rows > 1 and stride < K):
-        x2 = x2.contiguous()
-        stride = K
+    dx = _dtype(x)
+    x2, stride = _rows(x, K)
+    rows = x.numel() // K
+    oshape = shape[:-1] + (N,)
     if out is None:
-        out = torch.empty(shape[:-1] + (N,), dtype=out_dtype or x.dtype, device=x.device)
-    elif out.shape != shape[:-1] + (N,) or not out.is_contiguous() or out.device != x.device or \
+        out = torch.empty(oshape, dtype=out_dtype or x.dtype, device=x.device)
+    elif out.shape != oshape or not out.is_contiguous() or out.get_device() != index or \
             (out_dtype is not None and out.dtype != out_dtype):
         raise ValueError("out is not a dense [..., N] tensor of the result's type")
-    _call("dflash2_linear_w4", x.device, x2.data_ptr(), _dtype(x), stride if rows > 1 else K, rows,
-          w4.buf.data_ptr(), N, K, w4.group, w4.format, out.data_ptr(), _dtype(out))
+    _call("dflash2_linear_w4", index, x2.data_ptr(), dx, stride, rows, w4.ptr, N, K, w4.group,
+          w4.format, out.data_ptr(), _dtype(out))
     return out
 
 
 def _dynconv2_w4(x, x_prev, w4, out):
     if not w4.taps:
         raise ValueError("dynconv2 takes weights packed with taps=True")
-    if not x.is_cuda or x.device != w4.device or x_prev.device != w4.device:
+    index = w4.index
+    if x.get_device() != index or x_prev.get_device() != index:
         raise ValueError("x, x_prev and the weights are on one CUDA device")
     B, T, H = x.shape
     if H != w4.K or x_prev.shape != (B, H) or x_prev.dtype != x.dtype:
@@ -477,10 +485,10 @@ def _dynconv2_w4(x, x_prev, w4, out):
     if out is None:
         out = torch.empty_like(x)
     elif out.shape != x.shape or out.dtype != x.dtype or not out.is_contiguous() or \
-            out.device != x.device:
+            out.get_device() != index:
         raise ValueError("out is not a dense tensor like x")
-    _call("dflash2_dynconv2_w4", x.device, x.data_ptr(), x_prev.data_ptr(), w4.buf.data_ptr(),
-          w4.group, w4.format, _dtype(x), B, T, H, out.data_ptr())
+    _call("dflash2_dynconv2_w4", index, x.data_ptr(), x_prev.data_ptr(), w4.ptr, w4.group, w4.format,
+          _dtype(x), B, T, H, out.data_ptr())
     return out
 
 
@@ -489,6 +497,8 @@ GATE_LINEAR, GATE_SIGMOID = 0, 1
 
 def _rows(t, H):
     """t [..., H] as (tensor, row stride) of one run of rows."""
+    if t.is_contiguous():
+        return t, H
     t2 = t if t.dim() == 2 else t.reshape(-1, H)
     if t2.stride(1) != 1 or (t2.shape[0] > 1 and t2.stride(0) < H):
         t2 = t2.contiguous()
@@ -504,46 +514,50 @@ def norm_residual(res, y, w_post=None, w_pre=None, gate=None, gate_act=GATE_LINE
     y's shape (per token), or None; w_post, w_pre [H] or None; gate and weights of
     y's type.  Returns (r', h), or r' alone without w_pre.  out: (r', h) or r' to
     write to; r' may be res."""
-    H = y.shape[-1]
-    dev, dt = y.device, y.dtype
-    _cuda(res, y, gate, w_post, w_pre)
-    _same_device(dev, res, gate, w_post, w_pre)
-    if res.shape != y.shape:
+    shape, dt, index = y.shape, y.dtype, y.get_device()
+    H = shape[-1]
+    if index < 0 or res.get_device() != index:
+        raise ValueError("dflash2 calls take tensors of one CUDA device")
+    if res.shape != shape:
         raise ValueError("res and y have one shape")
-    for t in (gate, w_post, w_pre):
-        if t is not None and t.dtype != dt:
-            raise TypeError("the gate and the weights have y's type")
-    for w in (w_post, w_pre):
-        if w is not None and w.shape != (H,):
-            raise ValueError("norm weights are [H]")
+    dy, dr = _dtype(y), _dtype(res)
     y2, ys = _rows(y, H)
     r2, rs = _rows(res, H)
-    rows = y2.shape[0]
+    rows = y.numel() // H if H else 0
+    wp = [None, None]
+    keep = []
+    for i, w in enumerate((w_post, w_pre)):
+        if w is not None:
+            _like(w, dt, index)
+            if w.dim() != 1 or w.shape[0] != H:
+                raise ValueError("norm weights are [H]")
+            if not w.is_contiguous():
+                keep.append(w := w.contiguous())
+            wp[i] = w.data_ptr()
     gp, gs, rep = None, H, 1
     if gate is not None:
-        if gate.shape == (H,):
-            rep, g2 = max(rows, 1), gate.contiguous()
-        elif gate.shape == y.shape:
-            g2, gs = _rows(gate, H)
-        elif y.dim() == 3 and gate.shape == (y.shape[0], H):
-            rep = max(y.shape[1], 1)
-            g2, gs = _rows(gate, H)
+        _like(gate, dt, index)
+        gshape = gate.shape
+        if len(gshape) == 1 and gshape[0] == H:
+            rep = max(rows, 1)
+        elif gshape == shape:
+            pass
+        elif len(shape) == 3 and len(gshape) == 2 and gshape[0] == shape[0] and gshape[1] == H:
+            rep = max(shape[1], 1)
         else:
             raise ValueError("gate is [H], [B, H] or like y")
+        g2, gs = (gate.contiguous(), H) if len(gshape) == 1 else _rows(gate, H)
         gp = g2.data_ptr()
-    w_post = None if w_post is None else w_post.contiguous()
-    w_pre = None if w_pre is None else w_pre.contiguous()
     if out is None:
-        r_out = torch.empty(y.shape, dtype=res.dtype, device=dev)
-        h = torch.empty(y.shape, dtype=dt, device=dev) if w_pre is not None else None
+        r_out = torch.empty_like(res, memory_format=torch.contiguous_format)
+        h = torch.empty_like(y, memory_format=torch.contiguous_format) if w_pre is not None else None
     else:
         r_out, h = out if w_pre is not None else (out, None)
         for t, like in ((r_out, res), (h, y)):
-            if t is not None and (t.shape != y.shape or t.dtype != like.dtype or
-                                  not t.is_contiguous() or t.device != dev):
+            if t is not None and (t.shape != shape or t.dtype != like.dtype or
+                                  not t.is_contiguous() or t.get_device() != index):
                 raise ValueError("out is not a dense tensor like res (and y)")
-    _call("dflash2_norm_residual", dev, r2.data_ptr(), _dtype(res), rs, y2.data_ptr(), _dtype(y), ys,
-          gp, gs, rep, gate_act, None if w_post is None else w_post.data_ptr(),
-          None if w_pre is None else w_pre.data_ptr(), w_offset, scale, eps, rows, H,
-          r_out.data_ptr(), None if h is None else h.data_ptr())
+    _call("dflash2_norm_residual", index, r2.data_ptr(), dr, rs, y2.data_ptr(), dy, ys, gp, gs, rep,
+          gate_act, wp[0], wp[1], w_offset, scale, eps, rows, H, r_out.data_ptr(),
+          None if h is None else h.data_ptr())
     return r_out if h is None else (r_out, h)

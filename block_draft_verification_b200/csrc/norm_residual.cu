@@ -7,9 +7,8 @@
 // One pass over memory: a row's y and r are read once, kept in registers while
 // the sum of squares of y, then of r', is formed in fp32, and r' and h are
 // written once.  h is taken from r' before its rounding.  A row is worked on
-// by a group of threads sized to it, so that few rows still spread over the
-// device and many rows keep all of it streaming; rows too long for registers
-// are read again from cache (three passes).
+// by one CTA sized to it; rows too long for its registers are read again from
+// cache (three passes).
 #include <algorithm>
 
 #include "common.cuh"
@@ -29,42 +28,60 @@ struct NormArgs {
     int sigmoid;
 };
 
-// N consecutive elements widened to fp32 (vec: one 16-byte load, or two).
-template <typename T, int N>
-__device__ __forceinline__ void ld_n(const T* p, float (&v)[N]) {
-    if constexpr (sizeof(T) == 2) {
-        static_assert(N == 8, "bf16 vectors are 8 wide");
-        const uint4 q = *(const uint4*)p;
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < N / 4; ++i) {
-            const float4 q = *(const float4*)(p + 4 * i);
-            v[4 * i] = q.x, v[4 * i + 1] = q.y, v[4 * i + 2] = q.z, v[4 * i + 3] = q.w;
-        }
+// W consecutive elements as they are stored (W = 8: 16-byte loads, W = 1: one
+// element), widened to fp32 when used.
+template <typename T, int W>
+struct Pack;
+template <>
+struct Pack<__nv_bfloat16, 8> {
+    uint4 q;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { q = *(const uint4*)p; }
+    __device__ __forceinline__ float get(int i) const {
+        const uint32_t w = i < 2 ? q.x : i < 4 ? q.y : i < 6 ? q.z : q.w;
+        return __uint_as_float((i & 1) ? (w & 0xFFFF0000u) : (w << 16));
     }
-}
-template <typename T, int N>
-__device__ __forceinline__ void st_n(T* p, const float (&v)[N]) {
-    if constexpr (sizeof(T) == 2) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t*>(&b);
-        }
-        *(uint4*)p = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < N / 4; ++i)
-            *(float4*)(p + 4 * i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+};
+template <>
+struct Pack<float, 8> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = *(const float4*)p;
+        b = *(const float4*)(p + 4);
     }
+    __device__ __forceinline__ float get(int i) const {
+        const float4& v = i < 4 ? a : b;
+        return (i & 3) == 0 ? v.x : (i & 3) == 1 ? v.y : (i & 3) == 2 ? v.z : v.w;
+    }
+};
+template <>
+struct Pack<__nv_bfloat16, 1> {
+    __nv_bfloat16 q;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { q = *p; }
+    __device__ __forceinline__ float get(int) const { return __bfloat162float(q); }
+};
+template <>
+struct Pack<float, 1> {
+    float q;
+    __device__ __forceinline__ void load(const float* p) { q = *p; }
+    __device__ __forceinline__ float get(int) const { return q; }
+};
+__device__ __forceinline__ void store_pack(__nv_bfloat16* p, const float (&v)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    *(uint4*)p = make_uint4(w[0], w[1], w[2], w[3]);
 }
+__device__ __forceinline__ void store_pack(float* p, const float (&v)[8]) {
+    *(float4*)p = make_float4(v[0], v[1], v[2], v[3]);
+    *(float4*)(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store_pack(__nv_bfloat16* p, const float (&v)[1]) {
+    *p = __float2bfloat16_rn(v[0]);
+}
+__device__ __forceinline__ void store_pack(float* p, const float (&v)[1]) { *p = v[0]; }
 __device__ __forceinline__ float ld_1(const float* p) { return *p; }
 __device__ __forceinline__ float ld_1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 __device__ __forceinline__ void st_1(float* p, float v) { *p = v; }
@@ -89,56 +106,56 @@ __device__ __forceinline__ float block_sum(float v, float* buf) {
     return v;
 }
 
-// XT: y, gate, weights and h; RT: the residual.  V vectors of 8 per thread held
-// in registers (H <= 8 V blockDim, H a multiple of 8, 16-byte rows).
-template <typename XT, typename RT, int V>
+// XT: y, gate, weights and h; RT: the residual; a thread holds V packs of W
+// elements of the row (blockDim V W >= H; W = 8 wants H a multiple of 8 and
+// 16-byte rows, W = 1 takes any).  Everything a row needs from memory is
+// requested before its first sum.
+template <typename XT, typename RT, int W, int V>
 __global__ void __launch_bounds__(512) norm_residual_kernel(const NormArgs a) {
     __shared__ float buf[2][32];
-    const int n8 = (int)(a.H / 8);
+    const int np = (int)(a.H / W);
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const XT* y = (const XT*)a.y + row * a.y_stride;
         const RT* r = (const RT*)a.res + row * a.res_stride;
         const XT* g = a.gate ? (const XT*)a.gate + row / a.gate_rep * a.gate_stride : nullptr;
-        float vy[V][8], vr[V][8];
+        Pack<XT, W> py[V], pg[V];
+        Pack<RT, W> pr[V];
         float ss = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int q = threadIdx.x + i * blockDim.x;
-            if (q < n8) {
-                ld_n<XT, 8>(y + 8 * q, vy[i]);
-                ld_n<RT, 8>(r + 8 * q, vr[i]);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) ss = fmaf(vy[i][e], vy[i][e], ss);
+            if (q < np) {
+                py[i].load(y + W * q);
+                pr[i].load(r + W * q);
+                if (g) pg[i].load(g + W * q);
             }
         }
         float inv = a.alpha;
-        if (a.w_post) inv *= rsqrtf(block_sum(ss, buf[0]) / (float)a.H + a.eps);
+        if (a.w_post) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (threadIdx.x + i * blockDim.x < np)
+#pragma unroll
+                    for (int e = 0; e < W; ++e) ss = fmaf(py[i].get(e), py[i].get(e), ss);
+            inv *= rsqrtf(block_sum(ss, buf[0]) / (float)a.H + a.eps);
+        }
+        float vr[V][W];
         float s2 = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int q = threadIdx.x + i * blockDim.x;
-            if (q < n8) {
-                float f[8];
+            if (q < np) {
+                Pack<XT, W> pw;
+                if (a.w_post) pw.load((const XT*)a.w_post + W * q);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = inv;
-                if (a.w_post) {
-                    float w[8];
-                    ld_n<XT, 8>((const XT*)a.w_post + 8 * q, w);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) f[e] *= w[e] + a.w_offset;
-                }
-                if (g) {
-                    float w[8];
-                    ld_n<XT, 8>(g + 8 * q, w);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) f[e] *= act(w[e], a.sigmoid);
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    vr[i][e] = fmaf(f[e], vy[i][e], vr[i][e]);
+                for (int e = 0; e < W; ++e) {
+                    float f = inv;
+                    if (a.w_post) f *= pw.get(e) + a.w_offset;
+                    if (g) f *= act(pg[i].get(e), a.sigmoid);
+                    vr[i][e] = fmaf(f, py[i].get(e), pr[i].get(e));
                     s2 = fmaf(vr[i][e], vr[i][e], s2);
                 }
-                st_n<RT, 8>((RT*)a.res_out + row * a.H + 8 * q, vr[i]);
+                store_pack((RT*)a.res_out + row * a.H + W * q, vr[i]);
             }
         }
         if (a.w_pre) {
@@ -146,12 +163,13 @@ __global__ void __launch_bounds__(512) norm_residual_kernel(const NormArgs a) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int q = threadIdx.x + i * blockDim.x;
-                if (q < n8) {
-                    float w[8];
-                    ld_n<XT, 8>((const XT*)a.w_pre + 8 * q, w);
+                if (q < np) {
+                    Pack<XT, W> pw;
+                    pw.load((const XT*)a.w_pre + W * q);
+                    float o[W];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) w[e] = vr[i][e] * inv2 * (w[e] + a.w_offset);
-                    st_n<XT, 8>((XT*)a.h + row * a.H + 8 * q, w);
+                    for (int e = 0; e < W; ++e) o[e] = vr[i][e] * inv2 * (pw.get(e) + a.w_offset);
+                    store_pack((XT*)a.h + row * a.H + W * q, o);
                 }
             }
         }
@@ -215,20 +233,23 @@ namespace {
 template <typename XT, typename RT>
 int launch(const NormArgs& a, bool vec, cudaStream_t s) {
     const unsigned grid = (unsigned)std::min<int64_t>(a.rows, 1 << 30);
-    const int64_t n8 = a.H / 8;
-    if (vec && n8 <= 4 * 512) {
-        // a vector or two per thread: the loads of a row are all in flight at once
-        const int threads = (int)std::min<int64_t>(512, std::max<int64_t>(32, (n8 + 31) / 32 * 32));
-        const int v = (int)((n8 + threads - 1) / threads);
-        if (v <= 1)
-            norm_residual_kernel<XT, RT, 1><<<grid, threads, 0, s>>>(a);
-        else if (v <= 2)
-            norm_residual_kernel<XT, RT, 2><<<grid, threads, 0, s>>>(a);
+    // packs of a row; up to 512 threads take V of them each, all but evenly
+    const int64_t np = vec ? a.H / 8 : a.H;
+    auto threads = [&](int v) { return (int)(((np + v - 1) / v + 31) / 32 * 32); };
+    if (vec && np <= 4 * 512) {
+        if (np <= 512)
+            norm_residual_kernel<XT, RT, 8, 1><<<grid, threads(1), 0, s>>>(a);
+        else if (np <= 2 * 512)
+            norm_residual_kernel<XT, RT, 8, 2><<<grid, threads(2), 0, s>>>(a);
         else
-            norm_residual_kernel<XT, RT, 4><<<grid, threads, 0, s>>>(a);
+            norm_residual_kernel<XT, RT, 8, 4><<<grid, threads(4), 0, s>>>(a);
+    } else if (!vec && np <= 8 * 512) {
+        if (np <= 2 * 512)
+            norm_residual_kernel<XT, RT, 1, 4><<<grid, threads(4), 0, s>>>(a);
+        else
+            norm_residual_kernel<XT, RT, 1, 8><<<grid, threads(8), 0, s>>>(a);
     } else {
-        const int threads = (int)std::min<int64_t>(512, (a.H + 31) / 32 * 32);
-        norm_residual_any_kernel<XT, RT><<<grid, threads, 0, s>>>(a);
+        norm_residual_any_kernel<XT, RT><<<grid, 512, 0, s>>>(a);
     }
     return launch_status();
 }
