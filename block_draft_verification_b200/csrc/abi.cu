@@ -41,12 +41,14 @@ unsigned dfl_errors_trunc(int clear);
 unsigned dfl_errors_select_tc(int clear);
 unsigned dfl_errors_greedy_ee(int clear);
 unsigned dfl_errors_w4(int clear);
+unsigned dfl_errors_w4_tc(int clear);
 
 extern "C" unsigned dflash2_device_errors(int clear) {
-    const unsigned f[8] = {dfl_errors_topk(clear),      dfl_errors_verify(clear),
+    const unsigned f[9] = {dfl_errors_topk(clear),      dfl_errors_verify(clear),
                            dfl_errors_dynconv(clear),   dfl_errors_select(clear),
                            dfl_errors_trunc(clear),     dfl_errors_select_tc(clear),
-                           dfl_errors_greedy_ee(clear), dfl_errors_w4(clear)};
+                           dfl_errors_greedy_ee(clear), dfl_errors_w4(clear),
+                           dfl_errors_w4_tc(clear)};
     unsigned v = 0;
     for (unsigned x : f) {
         if (x == 0xFFFFFFFFu) return 0xFFFFFFFFu;

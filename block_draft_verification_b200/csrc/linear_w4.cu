@@ -24,6 +24,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "linear_w4.cuh"
 #include "stream.cuh"
 #include "w4.cuh"
 
@@ -540,16 +541,9 @@ using namespace dfl_host;
 
 namespace {
 
-// The device at hand and how many clusters of each size it holds at once, one
-// CTA per SM (of 148 SMs: 148, 74, 33 and 15 of size 1, 2, 4 and 8; larger
-// clusters fit a GPU's processing clusters less well).
-struct Dev {
-    int id;
-    int clusters[9];
-};
-bool device_info(Dev& d) {
+bool device_info(W4Dev& d) {
     static std::mutex mu;
-    static Dev known[64] = {};
+    static W4Dev known[64] = {};
     if (cudaGetDevice(&d.id) != cudaSuccess) return false;
     std::lock_guard<std::mutex> g(mu);
     if (d.id < 64 && known[d.id].clusters[1] > 0) {
@@ -585,7 +579,7 @@ struct W4Plan {
     bool offs;
     size_t smem;
 };
-W4Plan w4_plan(const W4Layout& L, int format, int64_t tokens, bool x_f32, bool y_f32, const Dev& d) {
+W4Plan w4_plan(const W4Layout& L, int format, int64_t tokens, bool x_f32, bool y_f32, const W4Dev& d) {
     W4Plan best{};
     int64_t best_cost = -1;
     const int planes = x_f32 ? 3 : 1;
@@ -702,8 +696,8 @@ int launch_fmt(const W4Args& a, const W4Plan& P, int format, int dev, cudaStream
     if (format & DFLASH2_W4_ZERO) return launch_group<XT, 1, OFFS>(a, P, dev, s);
     return launch_group<XT, 0, OFFS>(a, P, dev, s);
 }
-int launch_any(const W4Args& a, const W4Plan& P, int format, int dtype, int dev, cudaStream_t s) {
-    if (dtype == DFLASH2_F32) return launch_fmt<float, false>(a, P, format, dev, s);
+int launch_any(const W4Args& a, const W4Plan& P, int format, bool x_f32, int dev, cudaStream_t s) {
+    if (x_f32) return launch_fmt<float, false>(a, P, format, dev, s);
     return P.offs ? launch_fmt<__nv_bfloat16, true>(a, P, format, dev, s)
                   : launch_fmt<__nv_bfloat16, false>(a, P, format, dev, s);
 }
@@ -711,12 +705,25 @@ int launch_any(const W4Args& a, const W4Plan& P, int format, int dtype, int dev,
 constexpr int W4_FORMATS = DFLASH2_W4_ZERO | DFLASH2_W4_SCALE_F32 | DFLASH2_W4_TAPS;
 constexpr int64_t W4_MAX_TOKENS = 1 << 18;
 
-W4Args w4_args(const W4Layout& L, const W4Plan& P, const void* packed) {
+// A checked call: by token count and type to one of the two kernels.
+int run(const W4Call& c, cudaStream_t s) {
+    W4Dev d;
+    if (!device_info(d)) return DFLASH2_ECUDA;
+    if (!c.x_f32 && dfl_linear_w4_tc_ok(c)) return dfl_linear_w4_tc(c, d, s);
+    const W4Plan P = w4_plan(c.L, c.format, c.tokens, c.x_f32, !c.y_bf16, d);
     W4Args a{};
-    a.packed = (const uint8_t*)packed;
-    a.N = L.N;
-    a.K = L.K;
-    a.units = L.units;
+    a.packed = (const uint8_t*)c.packed;
+    a.N = c.L.N;
+    a.K = c.L.K;
+    a.units = c.L.units;
+    a.tokens = c.tokens;
+    a.x = c.x;
+    a.x_stride = c.x_stride;
+    a.x_vec = c.x_vec;
+    a.y = c.y;
+    a.y_bf16 = c.y_bf16;
+    a.x_prev = c.x_prev;
+    a.T = c.T;
     a.S = P.S;
     a.C = P.C;
     a.steps = P.steps;
@@ -729,7 +736,7 @@ W4Args w4_args(const W4Layout& L, const W4Plan& P, const void* packed) {
     a.xsum_off = P.xsum_off;
     a.part_off = P.part_off;
     a.counts_off = P.counts_off;
-    return a;
+    return launch_any(a, P, c.format, c.x_f32, d.id, s);
 }
 
 }  // namespace
@@ -770,19 +777,18 @@ extern "C" int dflash2_linear_w4(const void* x, int dtype, int64_t x_stride, int
     const int es = elem_size(dtype);
     if (!aligned(x, es) || !aligned(packed, 256) || !aligned(y, elem_size(out_dtype)))
         return DFLASH2_EALIGN;
-    Dev d;
-    if (!device_info(d)) return DFLASH2_ECUDA;
-    const W4Layout L = w4_layout(N, K, group, format);
-    const W4Plan P = w4_plan(L, format, tokens, dtype == DFLASH2_F32, out_dtype == DFLASH2_F32, d);
-    W4Args a = w4_args(L, P, packed);
-    a.x = x;
-    a.x_stride = x_stride;
-    a.x_vec = aligned(x, 16) && (tokens == 1 || x_stride * es % 16 == 0);
-    a.tokens = tokens;
-    a.y = y;
-    a.y_bf16 = out_dtype == DFLASH2_BF16;
-    cudaStream_t s = (cudaStream_t)stream;
-    return launch_any(a, P, format, dtype, d.id, s);
+    W4Call c{};
+    c.L = w4_layout(N, K, group, format);
+    c.format = format;
+    c.packed = packed;
+    c.x = x;
+    c.x_stride = x_stride;
+    c.tokens = tokens;
+    c.x_f32 = dtype == DFLASH2_F32;
+    c.x_vec = aligned(x, 16) && (tokens == 1 || x_stride * es % 16 == 0);
+    c.y = y;
+    c.y_bf16 = out_dtype == DFLASH2_BF16;
+    return run(c, (cudaStream_t)stream);
 }
 
 extern "C" int dflash2_dynconv2_w4(const void* x, const void* x_prev, const void* packed, int group,
@@ -797,23 +803,20 @@ extern "C" int dflash2_dynconv2_w4(const void* x, const void* x_prev, const void
     if (!x || !x_prev || !packed || !out) return DFLASH2_EINVAL;
     if (!aligned(x, 16) || !aligned(x_prev, 16) || !aligned(packed, 256) || !aligned(out, 16))
         return DFLASH2_EALIGN;
-    Dev d;
-    if (!device_info(d)) return DFLASH2_ECUDA;
-    const int64_t tokens = (int64_t)B * T;
-    const W4Layout L = w4_layout(2 * (int64_t)H, H, group, format);
-    const W4Plan P = w4_plan(L, format, tokens, dtype == DFLASH2_F32, dtype == DFLASH2_F32, d);
-    W4Args a = w4_args(L, P, packed);
-    a.x = x;
-    a.x_stride = H;
-    a.x_vec = 1;
-    a.x_prev = x_prev;
-    a.T = T;
-    a.tokens = tokens;
-    a.y = out;
-    a.y_bf16 = dtype == DFLASH2_BF16;
-    cudaStream_t s = (cudaStream_t)stream;
-    const int fmt = format & ~DFLASH2_W4_TAPS;
-    return launch_any(a, P, fmt, dtype, d.id, s);
+    W4Call c{};
+    c.L = w4_layout(2 * (int64_t)H, H, group, format);
+    c.format = format & ~DFLASH2_W4_TAPS;
+    c.packed = packed;
+    c.x = x;
+    c.x_stride = H;
+    c.tokens = (int64_t)B * T;
+    c.x_f32 = dtype == DFLASH2_F32;
+    c.x_vec = true;
+    c.y = out;
+    c.y_bf16 = dtype == DFLASH2_BF16;
+    c.x_prev = x_prev;
+    c.T = T;
+    return run(c, (cudaStream_t)stream);
 }
 
 unsigned dfl_errors_w4(int clear) {

@@ -1,0 +1,32 @@
+// linear_w4.cuh -- what the two kernels for products with 4-bit weights share on
+// the host: one call's arguments, checked, and the device they run on.
+#pragma once
+
+#include "w4.cuh"
+
+struct W4Call {
+    dfl::W4Layout L;
+    int format;           // without DFLASH2_W4_TAPS
+    const void* packed;
+    const void* x;
+    int64_t x_stride, tokens;
+    bool x_f32, x_vec;    // x_vec: rows of x start on 16 bytes
+    void* y;
+    bool y_bf16;
+    const void* x_prev;   // conv; NULL: linear
+    int T;                // conv: tokens per sequence
+};
+
+// The device at hand and how many clusters of each size it holds at once, one
+// CTA per SM (of 148 SMs: 148, 74, 33 and 15 of size 1, 2, 4 and 8; larger
+// clusters fit a GPU's processing clusters less well).
+struct W4Dev {
+    int id;
+    int clusters[9];
+};
+
+// Tokens from which the tensor-core kernel is the faster one.
+constexpr int64_t W4_TC_MIN_TOKENS = 16;
+
+bool dfl_linear_w4_tc_ok(const W4Call& c);
+int dfl_linear_w4_tc(const W4Call& c, const W4Dev& d, cudaStream_t s);

@@ -1,0 +1,580 @@
+// linear_w4_tc.cu -- the products of linear_w4.cu for more tokens than a few, on
+// the tensor cores (tcgen05): bf16 activations, any output type.
+//
+// A tile is 128 weight rows (four units) by up to 128 tokens.  Its K loop, one
+// packed step (64 or 128 k) at a time:
+//   warp 0       bulk copies of the four units' packed steps into the W ring, TMA
+//                of the tokens' x (64 k boxes, 128-byte swizzle) into the X ring
+//   warps 2-9    codes to exact bf16 integers q - zero, stored as the K-major,
+//                128-byte swizzled A tile
+//   warp 1       tcgen05.mma (M = 128, N = tokens, K = 16) of a group's k into one
+//                of two TMEM accumulators
+//   warps 10-17  tcgen05.ld of the group's sums, times the row's scale, added to
+//                fp32 sums in registers while the next group's MMAs run
+// so the weights are never rounded: a group's integer-weighted sums come out of
+// the tensor core and the scale multiplies them in fp32.  The scaling costs 128 x
+// N fused multiply-adds a group beside 128 x N x group on the tensor core.
+//
+// Tiles are taken by clusters of S CTAs that split K; the sums meet in
+// distributed shared memory in rank order: no workspace, no atomics.  S is the
+// one that leaves the SMs least idle.  Every wait is bounded (stream.cuh); on a
+// timeout a flag is set, the roles leave their loops, copies and MMAs in flight
+// are waited for (bounded) and TMEM is released.
+#include <cooperative_groups.h>
+#include <cuda.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "common.cuh"
+#include "linear_w4.cuh"
+#include "stream.cuh"
+#include "tc.cuh"
+#include "w4.cuh"
+
+namespace dfl {
+
+namespace cg = cooperative_groups;
+
+constexpr int TW_ROWS = 128;            // weight rows per tile: four units
+constexpr int TW_DEQ = 8, TW_SUM = 8;   // warps
+constexpr int TW_THREADS = 32 * (2 + TW_DEQ + TW_SUM);
+constexpr int TW_SUB = TW_ROWS * 128;   // bytes of 64 k of A
+
+struct W4TcArgs {
+    const uint8_t* packed;
+    int64_t units, tokens, n_rows;  // n_rows: rows of W
+    int64_t ld;                     // linear: N; conv: H
+    int steps, S, C, tt;            // K steps, cluster size, clusters, token tiles
+    int64_t tiles;
+    void* y;
+    int y_bf16;
+    const __nv_bfloat16* x;         // conv
+    const __nv_bfloat16* x_prev;    // conv; NULL: linear
+    int T;
+};
+
+// Stages of the rings, by chunks per step.
+__host__ __device__ constexpr int tw_a_stages(int kb) { return kb == 2 ? 2 : 4; }
+__host__ __device__ constexpr int tw_w_stages(int kb) { return kb == 2 ? 3 : 5; }
+__host__ __device__ constexpr int tw_w_stage(int kb, int sg, int fmt) {
+    return 4 * (kb * W4_CHUNK_BYTES + sg * w4_scale_bytes(fmt));
+}
+// A ring, X ring, the tile's sums, W ring, barriers, and 1 KB to align the start.
+__host__ __device__ constexpr int tw_smem(int n, int kb, int sg, int fmt) {
+    return 1024 + tw_a_stages(kb) * kb * (TW_SUB + n * 128) + n * TW_ROWS * 4 +
+           tw_w_stages(kb) * tw_w_stage(kb, sg, fmt) + 512;
+}
+
+__device__ __forceinline__ void tw_load_x(uint32_t dst, const CUtensorMap* map, int k, int tok,
+                                          uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(k), "r"(tok), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void cluster_arrive(uint32_t bar, int rank) {
+    asm volatile(
+        "{\n\t.reg .b32 r;\n\t"
+        "mapa.shared::cluster.u32 r, %0, %1;\n\t"
+        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n\t}" ::"r"(bar),
+        "r"(rank)
+        : "memory");
+}
+__device__ __forceinline__ bool cluster_wait(uint32_t bar, uint32_t parity) {
+    const uint64_t t0 = global_ns();
+    while (true) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(bar), "r"(parity), "r"(SUSPEND_NS)
+            : "memory");
+        if (done) return true;
+        if (global_ns() - t0 > WAIT_NS) return false;
+    }
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr, int rank) {
+    float v;
+    asm volatile(
+        "{\n\t.reg .b32 r;\n\t"
+        "mapa.shared::cluster.u32 r, %1, %2;\n\t"
+        "ld.shared::cluster.f32 %0, [r];\n\t}"
+        : "=f"(v)
+        : "r"(addr), "r"(rank)
+        : "memory");
+    return v;
+}
+// 32 lanes x 16 consecutive fp32 columns, no wait.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+// NTOK: tokens per tile (32, 64, 128); FMT: scale format; G32: groups of 32, two
+// per step; KB: chunks per step.
+template <int NTOK, int FMT, bool G32, int KB>
+__global__ void __launch_bounds__(TW_THREADS, 1)
+    linear_w4_tc_kernel(const __grid_constant__ CUtensorMap map_x, const W4TcArgs a) {
+    constexpr int SG = G32 ? 2 : 1;
+    constexpr int SB = w4_scale_bytes(FMT), LB = SB / 8;
+    constexpr int STEP = KB * W4_CHUNK_BYTES + SG * SB;
+    constexpr int NA = tw_a_stages(KB), NW = tw_w_stages(KB);
+    constexpr int WST = tw_w_stage(KB, SG, FMT);
+    constexpr int XSUB = NTOK * 128;       // bytes of 64 k of x
+    constexpr int NC = NTOK / 2;           // columns per summing warp
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sa = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t* sx = sa + NA * KB * TW_SUB;
+    float* sp = (float*)(sx + NA * KB * XSUB);  // [token][row] sums of a finished tile
+    uint8_t* sw = (uint8_t*)sp + NTOK * TW_ROWS * 4;
+    uint64_t* bars = (uint64_t*)(sw + NW * WST);
+    uint32_t* s_tmem = (uint32_t*)(bars + 40);
+    // a summing warp gave up before a tile's first, second barrier: each is set on
+    // one side of a barrier and read on the other, so all eight leave together
+    volatile int* s_fail = (volatile int*)(s_tmem + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = blockIdx.x % a.S, cl = blockIdx.x / a.S;
+    const int k0 = (int)((int64_t)a.steps * rank / a.S);
+    const int nst = (int)((int64_t)a.steps * (rank + 1) / a.S) - k0;
+
+    const uint32_t wfull = smem_u32(bars), wempty = wfull + 8 * NW, xfull = wempty + 8 * NW,
+                   afull = xfull + 8 * NA, aempty = afull + 8 * NA, tfull = aempty + 8 * NA,
+                   tempty = tfull + 16, mdone = tempty + 16, pready = mdone + 8,
+                   pfree = pready + 8;  // aempty frees the X stage too: one commit covers both
+    static_assert(2 * NW + 3 * NA + 7 <= 40, "barriers");
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NW; ++i) {
+            mbar_init(wfull + 8 * i, 1);
+            mbar_init(wempty + 8 * i, TW_DEQ + TW_SUM);
+        }
+        for (int i = 0; i < NA; ++i) {
+            mbar_init(xfull + 8 * i, 1);
+            mbar_init(afull + 8 * i, TW_DEQ);
+            mbar_init(aempty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(tfull + 8 * i, 1);
+            mbar_init(tempty + 8 * i, TW_SUM);
+        }
+        mbar_init(mdone, 1);
+        mbar_init(pready, (uint32_t)a.S);
+        mbar_init(pfree, (uint32_t)a.S);
+        mbar_fence_init();
+        s_fail[0] = s_fail[1] = 0;
+    }
+    constexpr uint32_t NCOLS = 2 * NTOK;  // two accumulators
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(s_tmem)),
+                     "r"(NCOLS));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (a.S > 1) cg::this_cluster().sync();  // the barriers of every CTA are set up
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---------------- producer
+            int i = 0;
+            bool ok = true;
+            for (int64_t tile = cl; tile < a.tiles && ok; tile += a.C) {
+                const int64_t rt = tile / a.tt, u0 = rt * 4;
+                const int tok0 = (int)(tile - rt * a.tt) * NTOK;
+                const int nu = (int)min((int64_t)4, a.units - u0);
+                for (int s = 0; s < nst; ++s, ++i) {
+                    const int w = i % NW, x = i % NA;
+                    if ((i >= NW && !mbar_wait(wempty + 8 * w, (i / NW - 1) & 1)) ||
+                        (i >= NA && !mbar_wait(aempty + 8 * x, (i / NA - 1) & 1))) {
+                        atomicOr(&g_dev_err, ERR_PRODUCER);
+                        ok = false;
+                        break;
+                    }
+                    mbar_expect_tx(wfull + 8 * w, (uint32_t)(nu * STEP));
+                    for (int u = 0; u < nu; ++u)
+                        bulk_g2s_nx(smem_u32(sw + w * WST + u * STEP),
+                                    a.packed + ((u0 + u) * a.steps + k0 + s) * STEP, STEP,
+                                    wfull + 8 * w);
+                    mbar_expect_tx(xfull + 8 * x, (uint32_t)(KB * XSUB));
+#pragma unroll
+                    for (int c = 0; c < KB; ++c)
+                        tw_load_x(smem_u32(sx + (x * KB + c) * XSUB), &map_x,
+                                  ((k0 + s) * KB + c) * W4_CHUNK, tok0, xfull + 8 * x);
+                }
+            }
+            // the last copies have landed before the CTA may leave
+            for (int q = i > NW ? i - NW : 0; q < i; ++q)
+                if (!mbar_wait(wfull + 8 * (q % NW), (q / NW) & 1)) atomicOr(&g_dev_err, ERR_DRAIN);
+            for (int q = i > NA ? i - NA : 0; q < i; ++q)
+                if (!mbar_wait(xfull + 8 * (q % NA), (q / NA) & 1)) atomicOr(&g_dev_err, ERR_DRAIN);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // ---------------- MMA issuer
+            int i = 0, j = 0;
+            bool ok = true;
+            for (int64_t tile = cl; tile < a.tiles && ok; tile += a.C) {
+                const int64_t left = a.tokens - (tile % a.tt) * NTOK;
+                const uint32_t idesc =
+                    instr_desc(TW_ROWS, (int)min((int64_t)NTOK, (left + 15) / 16 * 16));
+                for (int s = 0; s < nst && ok; ++s, ++i) {
+                    const int st = i % NA;
+                    if (!mbar_wait(afull + 8 * st, (i / NA) & 1) ||
+                        !mbar_wait(xfull + 8 * st, (i / NA) & 1)) {
+                        atomicOr(&g_dev_err, ERR_MMA);
+                        ok = false;
+                        break;
+                    }
+#pragma unroll
+                    for (int h = 0; h < SG; ++h, ++j) {
+                        const int buf = j & 1;
+                        if (ok && j >= 2 && !mbar_wait(tempty + 8 * buf, ((j - 2) >> 1) & 1)) {
+                            atomicOr(&g_dev_err, ERR_MMA);
+                            ok = false;
+                        }
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t d = tmem + (uint32_t)(buf * NTOK);
+                        constexpr int KK = KB * 4 / SG;  // K = 16 products of a group's part
+#pragma unroll
+                        for (int kk = 0; kk < KK; ++kk) {
+                            const int q = h * KK + kk;
+                            const uint32_t ao = smem_u32(sa + (st * KB + (q >> 2)) * TW_SUB) + (q & 3) * 32;
+                            const uint32_t xo = smem_u32(sx + (st * KB + (q >> 2)) * XSUB) + (q & 3) * 32;
+                            mma_bf16(d, smem_desc(ao), smem_desc(xo), idesc, kk > 0 ? 1u : 0u);
+                        }
+                        mma_commit(tfull + 8 * buf);
+                    }
+                    if (ok) mma_commit(aempty + 8 * st);
+                }
+            }
+            mma_commit(mdone);  // every MMA this thread issued has completed once this fires
+        }
+    } else if (warp < 2 + TW_DEQ) {
+        // ---------------- codes to operands: half blocks (16 rows x 64 k) of a step
+        const int d = warp - 2;
+        const int r = lane >> 2, c = lane & 3;
+        const bool odd = (r & 1) != 0;  // odd rows store their second half first: the
+                                        // eight lanes of a store then hit all banks
+        int i = 0;
+        bool ok = true;
+        for (int64_t tile = cl; tile < a.tiles && ok; tile += a.C) {
+            for (int s = 0; s < nst; ++s, ++i) {
+                const int w = i % NW, st = i % NA;
+                if (!mbar_wait(wfull + 8 * w, (i / NW) & 1) ||
+                    (i >= NA && !mbar_wait(aempty + 8 * st, (i / NA - 1) & 1))) {
+                    if (lane == 0) atomicOr(&g_dev_err, ERR_EPILOGUE);
+                    ok = false;
+                    break;
+                }
+#pragma unroll
+                for (int m = 0; m < KB; ++m) {
+                    // of the step's 8 KB half blocks: unit u, half b, chunk m
+                    const int u = d >> 1, b = d & 1;
+                    const uint8_t* blk = sw + w * WST + u * STEP;
+                    const uint4 v = *(const uint4*)(blk + m * W4_CHUNK_BYTES + b * 512 + lane * 16);
+                    W4Scale<FMT> zs[SG];
+                    if constexpr (FMT != 0) {
+#pragma unroll
+                        for (int h = 0; h < SG; ++h) zs[h].load(blk + KB * W4_CHUNK_BYTES + h * SB + r * LB);
+                    }
+                    uint8_t* dst = sa + (st * KB + m) * TW_SUB + (u * 32 + b * 16 + r) * 128;
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
+                        const bool second = odd != (hh == 1);  // which half of the row's 64 k
+                        const int off = ((4 * (second ? 1 : 0) + c) ^ r) * 16;
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {  // rows r and r + 8
+                            const uint32_t word = q == 0 ? (second ? v.y : v.x) : (second ? v.w : v.z);
+                            uint32_t zz = zs[0].zero2(2 * b + q);
+                            if constexpr (G32 && FMT != 0) {
+                                const uint32_t z1 = zs[SG - 1].zero2(2 * b + q);
+                                zz = second ? z1 : zz;
+                            }
+                            *(uint4*)(dst + q * 1024 + off) =
+                                make_uint4(w4_pair_exact(word, 0, zz), w4_pair_exact(word, 1, zz),
+                                           w4_pair_exact(word, 2, zz), w4_pair_exact(word, 3, zz));
+                        }
+                    }
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(afull + 8 * st);
+                    mbar_arrive(wempty + 8 * w);
+                }
+            }
+        }
+    } else {
+        // ---------------- scaling and sums
+        const int q = warp & 3;                     // TMEM lanes 32 q .. 32 q + 31 = unit q
+        const int half = (warp - 2 - TW_DEQ) >> 2;  // columns half * NC ..
+        const int e = threadIdx.x - 32 * (2 + TW_DEQ);
+        const uint32_t tb = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(half * NC);
+        const int srow = (lane & 7) * LB, sj = lane >> 3;  // this row's scale
+        int i = 0, j = 0, ntile = 0;
+        bool ok = true;
+        for (int64_t tile = cl; tile < a.tiles; tile += a.C, ++ntile) {
+            const int64_t rt = tile / a.tt;
+            const int64_t tok0 = (tile - rt * a.tt) * NTOK;
+            const int ntok = (int)min((int64_t)NTOK, a.tokens - tok0);
+            float acc[NC];
+#pragma unroll
+            for (int n = 0; n < NC; ++n) acc[n] = 0.0f;
+            for (int s = 0; s < nst && ok; ++s, ++i) {
+                const int w = i % NW;
+                float sc[SG];
+                ok = mbar_wait(wfull + 8 * w, (i / NW) & 1);
+                if (ok) {
+                    const uint8_t* p = sw + w * WST + q * STEP + KB * W4_CHUNK_BYTES + srow;
+#pragma unroll
+                    for (int h = 0; h < SG; ++h) {
+                        if constexpr ((FMT & DFLASH2_W4_SCALE_F32) != 0)
+                            sc[h] = ((const float*)(p + h * SB))[sj];
+                        else
+                            sc[h] = __uint_as_float((uint32_t)((const unsigned short*)(p + h * SB))[sj] << 16);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(wempty + 8 * w);
+                }
+#pragma unroll
+                for (int h = 0; h < SG; ++h, ++j) {
+                    const int buf = j & 1;
+                    ok = ok && mbar_wait(tfull + 8 * buf, (j >> 1) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t ta = tb + (uint32_t)(buf * NTOK);
+#pragma unroll
+                    for (int n = 0; n < NC; n += 16) {
+                        if (half * NC + n < ntok) {  // the same for the whole warp
+                            uint32_t v[16];
+                            tmem_ld16(ta + n, v);
+                            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                            for (int z = 0; z < 16; ++z)
+                                acc[n + z] = fmaf(sc[h], __uint_as_float(v[z]), acc[n + z]);
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(tempty + 8 * buf);
+                }
+            }
+            // the tile's sums of this CTA's K, then of the cluster's
+            if (ok && a.S > 1 && ntile > 0) ok = cluster_wait(pfree, (ntile - 1) & 1);
+            if (!ok) {
+                atomicOr(&g_dev_err, (unsigned)ERR_EPILOGUE);
+                s_fail[0] = 1;
+            } else {
+#pragma unroll
+                for (int n = 0; n < NC; ++n)
+                    sp[(half * NC + n) * TW_ROWS + 32 * q + lane] = acc[n];
+            }
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            if (s_fail[0]) break;
+            if (a.S > 1) {
+                if (e < a.S) cluster_arrive(pready, e);
+                ok = cluster_wait(pready, ntile & 1);
+                if (!ok) {
+                    atomicOr(&g_dev_err, (unsigned)ERR_EPILOGUE);
+                    s_fail[1] = 1;
+                }
+            }
+            // this CTA writes its share of the tokens
+            const int t0 = NTOK * rank / a.S, t1 = min(NTOK * (rank + 1) / a.S, ntok);
+            const uint32_t spu = smem_u32(sp);
+            auto sum_at = [&](int row, int t) {
+                const int o = t * TW_ROWS + row;
+                if (a.S == 1) return sp[o];
+                float v = 0.0f;
+                for (int k = 0; k < a.S; ++k) v += ld_cluster(spu + 4 * o, k);
+                return v;
+            };
+            if (ok) {
+                if (!a.x_prev) {
+                    const int64_t n = rt * TW_ROWS + (e & 127);
+                    if (n < a.n_rows)
+                        for (int t = t0 + (e >> 7); t < t1; t += 2) {
+                            const float v = sum_at(e & 127, t);
+                            const int64_t o = (tok0 + t) * a.ld + n;
+                            if (a.y_bf16)
+                                ((__nv_bfloat16*)a.y)[o] = __float2bfloat16_rn(v);
+                            else
+                                ((float*)a.y)[o] = v;
+                        }
+                } else {
+                    // a and b of a channel: rows 8 apart (w4_pack, taps)
+                    const int cl64 = e & 63, row = (cl64 >> 3) * 16 + (cl64 & 7);
+                    const int64_t ch = rt * 64 + cl64;
+                    if (ch < a.ld)
+                        for (int t = t0 + (e >> 6); t < t1; t += 4) {
+                            const int64_t tok = tok0 + t;
+                            const float av = sum_at(row, t), bv = sum_at(row + 8, t);
+                            const float xc = __bfloat162float(a.x[tok * a.ld + ch]);
+                            const float xp = __bfloat162float(
+                                tok % a.T == 0 ? a.x_prev[tok / a.T * a.ld + ch] : a.x[(tok - 1) * a.ld + ch]);
+                            ((__nv_bfloat16*)a.y)[tok * a.ld + ch] =
+                                __float2bfloat16_rn(fmaf(bv, xp, fmaf(av, xc, xc)));
+                        }
+                }
+            }
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            if (s_fail[1]) break;
+            if (a.S > 1 && e < a.S) cluster_arrive(pfree, e);
+        }
+    }
+    __syncthreads();
+    if (warp == 1) {
+        if (!mbar_wait(mdone, 0) && lane == 0) atomicOr(&g_dev_err, ERR_DRAIN);
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(NCOLS));
+    }
+    if (a.S > 1) cg::this_cluster().sync();  // the others may still read this CTA's sums
+}
+
+}  // namespace dfl
+
+using namespace dfl;
+
+namespace {
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn() {
+    static EncodeTiledFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        return cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
+                           cudaSuccess &&
+                       q == cudaDriverEntryPointSuccess
+                   ? (EncodeTiledFn)p
+                   : (EncodeTiledFn) nullptr;
+    }();
+    return fn;
+}
+
+template <int NTOK, int FMT, bool G32, int KB>
+int launch(const CUtensorMap& map, const W4TcArgs& a, int dev, cudaStream_t s) {
+    constexpr int smem = tw_smem(NTOK, KB, G32 ? 2 : 1, FMT);
+    static_assert(smem <= 227 * 1024, "shared memory of a CTA");
+    auto* k = linear_w4_tc_kernel<NTOK, FMT, G32, KB>;
+    {
+        static std::mutex mu;
+        static bool attr_set[64] = {};
+        std::lock_guard<std::mutex> g(mu);
+        if (dev >= 64 || !attr_set[dev]) {
+            if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+                return DFLASH2_ECUDA;
+            if (dev < 64) attr_set[dev] = true;
+        }
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.S * a.C));
+    cfg.blockDim = dim3(TW_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)a.S;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, map, a) == cudaSuccess ? DFLASH2_OK
+                                                              : (cudaGetLastError(), DFLASH2_ECUDA);
+}
+template <int NTOK, int FMT>
+int launch_group(const CUtensorMap& map, const W4TcArgs& a, const W4Layout& L, int dev, cudaStream_t s) {
+    if (L.kb == 2) return launch<NTOK, FMT, false, 2>(map, a, dev, s);
+    return L.sg == 2 ? launch<NTOK, FMT, true, 1>(map, a, dev, s)
+                     : launch<NTOK, FMT, false, 1>(map, a, dev, s);
+}
+template <int NTOK>
+int launch_fmt(const CUtensorMap& map, const W4TcArgs& a, const W4Layout& L, int format, int dev,
+               cudaStream_t s) {
+    if (format & DFLASH2_W4_SCALE_F32) return launch_group<NTOK, 2>(map, a, L, dev, s);
+    if (format & DFLASH2_W4_ZERO) return launch_group<NTOK, 1>(map, a, L, dev, s);
+    return launch_group<NTOK, 0>(map, a, L, dev, s);
+}
+
+}  // namespace
+
+bool dfl_linear_w4_tc_ok(const W4Call& c) {
+    return c.x_vec && c.tokens > W4_TC_MIN_TOKENS && encode_fn() != nullptr;
+}
+
+int dfl_linear_w4_tc(const W4Call& c, const W4Dev& d, cudaStream_t s) {
+    const W4Layout& L = c.L;
+    const int ntok = c.tokens <= 32 ? 32 : c.tokens <= 64 ? 64 : 128;
+    W4TcArgs a{};
+    a.packed = (const uint8_t*)c.packed;
+    a.units = L.units;
+    a.tokens = c.tokens;
+    a.n_rows = L.N;
+    a.ld = c.x_prev ? L.K : L.N;
+    a.steps = L.steps;
+    a.tt = (int)((c.tokens + ntok - 1) / ntok);
+    a.tiles = (L.units + 3) / 4 * a.tt;
+    a.y = c.y;
+    a.y_bf16 = c.y_bf16;
+    a.x = (const __nv_bfloat16*)c.x;
+    a.x_prev = (const __nv_bfloat16*)c.x_prev;
+    a.T = c.T;
+    // Cluster size: rounds of tiles times the length of one, in cycles: a step
+    // takes the longest of its MMAs (N / 2 cycles each), its weights' share of
+    // memory bandwidth (23 bytes a cycle and SM) and its instructions (codes, and
+    // N multiply-adds per summing warp and group); a tile's end about 2,000 more,
+    // and another 2,000 where sums cross CTAs.
+    const int64_t mma = (int64_t)L.kb * 4 * (ntok / 2), mem = 4 * L.step_bytes / 23;
+    const int64_t ins = (int64_t)L.kb * 140 + L.sg * (ntok + 60);
+    const int64_t step = std::max(mma, std::max(mem, ins));
+    int64_t best = -1;
+    for (int S = 1; S <= 8 && S <= L.steps; S *= 2) {
+        const int C = (int)std::min<int64_t>(a.tiles, d.clusters[S]);
+        const int64_t cost = ((a.tiles + C - 1) / C) *
+                                 ((L.steps + S - 1) / S * step + 1000 + 8 * ntok + (S > 1 ? 2000 : 0));
+        if (best < 0 || cost < best) {
+            best = cost;
+            a.S = S;
+            a.C = C;
+        }
+    }
+    CUtensorMap map;
+    cuuint64_t dims[2] = {(cuuint64_t)L.K, (cuuint64_t)c.tokens};
+    cuuint64_t strides[1] = {(cuuint64_t)(c.tokens > 1 ? c.x_stride : L.K) * 2};
+    cuuint32_t box[2] = {W4_CHUNK, (cuuint32_t)ntok};
+    cuuint32_t estr[2] = {1, 1};
+    if (encode_fn()(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(c.x), dims, strides,
+                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return DFLASH2_ECUDA;
+    if (ntok == 32) return launch_fmt<32>(map, a, L, c.format, d.id, s);
+    if (ntok == 64) return launch_fmt<64>(map, a, L, c.format, d.id, s);
+    return launch_fmt<128>(map, a, L, c.format, d.id, s);
+}
+
+unsigned dfl_errors_w4_tc(int clear) {
+    unsigned v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_dev_err, sizeof v) != cudaSuccess) return 0xFFFFFFFFu;
+    if (clear && v) {
+        unsigned z = 0;
+        cudaMemcpyToSymbol(g_dev_err, &z, sizeof z);
+    }
+    return v;
+}
