@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const uint8_t* __restrict_
             uint8_t* dst = packed + blk * L.step_bytes + L.kb * W4_CHUNK_BYTES + h * sbytes +
                            (size_t)g8 * (sbytes / 8);
             const unsigned short z16 =
-                (unsigned short)(0x4300u + (in ? zero_at(source(row), g) : 8u));
+                (unsigned short)(0x4180u + ((in ? zero_at(source(row), g) : 8u) << 3));
             if (f32s) {
                 ((float*)dst)[j] = in ? ((const float*)scale)[src] : 0.0f;
                 ((unsigned short*)(dst + 16))[j] = z16;

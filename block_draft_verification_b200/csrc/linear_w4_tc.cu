@@ -1,15 +1,16 @@
 // linear_w4_tc.cu -- the products of linear_w4.cu for more tokens than a few, on
 // the tensor cores (tcgen05): bf16 activations, any output type.
 //
-// A tile is 128 weight rows (four units) by up to 128 tokens.  Its K loop, one
-// packed step (64 or 128 k) at a time:
-//   warp 0       bulk copies of the four units' packed steps into the W ring, TMA
-//                of the tokens' x (64 k boxes, 128-byte swizzle) into the X ring
-//   warps 2-9    codes to exact bf16 integers q - zero, stored as the K-major,
-//                128-byte swizzled A tile
+// A tile is 128 weight rows (four units) by up to 128 tokens.  Its K loop:
+//   warp 0       bulk copies of the four units' packed steps (64 or 128 k) into the
+//                W ring, TMA of the tokens' x (64 k boxes, 128-byte swizzle) into
+//                the X ring
+//   warps 4-19   codes to exact bf16 integers q - zero, stored as the K-major,
+//                128-byte swizzled A tile of a 64 k chunk; the two halves of these
+//                warps take chunks in turn
 //   warp 1       tcgen05.mma (M = 128, N = tokens, K = 16) of a group's k into one
 //                of two TMEM accumulators
-//   warps 10-17  tcgen05.ld of the group's sums, times the row's scale, added to
+//   warps 20-27  tcgen05.ld of the group's sums, times the row's scale, added to
 //                fp32 sums in registers while the next group's MMAs run
 // so the weights are never rounded: a group's integer-weighted sums come out of
 // the tensor core and the scale multiplies them in fp32.  The scaling costs 128 x
@@ -37,9 +38,12 @@ namespace dfl {
 namespace cg = cooperative_groups;
 
 constexpr int TW_ROWS = 128;            // weight rows per tile: four units
-constexpr int TW_DEQ = 8, TW_SUM = 8;   // warps
-constexpr int TW_THREADS = 32 * (2 + TW_DEQ + TW_SUM);
+constexpr int TW_DEQ = 16, TW_SUM = 8;  // warps
+constexpr int TW_THREADS = 32 * (4 + TW_DEQ + TW_SUM);
 constexpr int TW_SUB = TW_ROWS * 128;   // bytes of 64 k of A
+constexpr int TW_NA = 4;                // chunks of A, and of x, in their rings
+// Registers: 896 threads are launched with 72 each; 128 x 40 + 512 x 56 + 256 x
+// 112 = 62,464 of the 64,512 are in use after the split.
 
 struct W4TcArgs {
     const uint8_t* packed;
@@ -48,21 +52,20 @@ struct W4TcArgs {
     int steps, S, C, tt;            // K steps, cluster size, clusters, token tiles
     int64_t tiles;
     void* y;
-    int y_bf16;
+    int y_bf16, y_vec;              // y_vec: four rows of a token may be stored at once
     const __nv_bfloat16* x;         // conv
     const __nv_bfloat16* x_prev;    // conv; NULL: linear
     int T;
 };
 
-// Stages of the rings, by chunks per step.
-__host__ __device__ constexpr int tw_a_stages(int kb) { return kb == 2 ? 2 : 4; }
+// Steps in the W ring.
 __host__ __device__ constexpr int tw_w_stages(int kb) { return kb == 2 ? 3 : 5; }
 __host__ __device__ constexpr int tw_w_stage(int kb, int sg, int fmt) {
     return 4 * (kb * W4_CHUNK_BYTES + sg * w4_scale_bytes(fmt));
 }
 // A ring, X ring, the tile's sums, W ring, barriers, and 1 KB to align the start.
 __host__ __device__ constexpr int tw_smem(int n, int kb, int sg, int fmt) {
-    return 1024 + tw_a_stages(kb) * kb * (TW_SUB + n * 128) + n * TW_ROWS * 4 +
+    return 1024 + TW_NA * (TW_SUB + n * 128) + n * TW_ROWS * 4 +
            tw_w_stages(kb) * tw_w_stage(kb, sg, fmt) + 512;
 }
 
@@ -97,19 +100,28 @@ __device__ __forceinline__ bool cluster_wait(uint32_t bar, uint32_t parity) {
         if (global_ns() - t0 > WAIT_NS) return false;
     }
 }
-__device__ __forceinline__ float ld_cluster(uint32_t addr, int rank) {
-    float v;
+// (volatile, so after the wait for the sums; no memory clobber, so that several
+// are in flight)
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr, int rank) {
+    float4 v;
     asm volatile(
         "{\n\t.reg .b32 r;\n\t"
-        "mapa.shared::cluster.u32 r, %1, %2;\n\t"
-        "ld.shared::cluster.f32 %0, [r];\n\t}"
-        : "=f"(v)
-        : "r"(addr), "r"(rank)
-        : "memory");
+        "mapa.shared::cluster.u32 r, %4, %5;\n\t"
+        "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [r];\n\t}"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+        : "r"(addr), "r"(rank));
     return v;
 }
-// 32 lanes x 16 consecutive fp32 columns, no wait.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+__device__ __forceinline__ void unpack4(uint2 q, float (&v)[4]) {
+    v[0] = __uint_as_float(q.x << 16), v[1] = __uint_as_float(q.x & 0xFFFF0000u);
+    v[2] = __uint_as_float(q.y << 16), v[3] = __uint_as_float(q.y & 0xFFFF0000u);
+}
+__device__ __forceinline__ uint2 pack4(const float (&v)[4]) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+    return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+// 32 lanes x N consecutive fp32 columns, no wait.
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
         "%14,%15}, [%16];"
@@ -127,14 +139,14 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
     constexpr int SG = G32 ? 2 : 1;
     constexpr int SB = w4_scale_bytes(FMT), LB = SB / 8;
     constexpr int STEP = KB * W4_CHUNK_BYTES + SG * SB;
-    constexpr int NA = tw_a_stages(KB), NW = tw_w_stages(KB);
+    constexpr int NA = TW_NA, NW = tw_w_stages(KB);
     constexpr int WST = tw_w_stage(KB, SG, FMT);
     constexpr int XSUB = NTOK * 128;       // bytes of 64 k of x
     constexpr int NC = NTOK / 2;           // columns per summing warp
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sa = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    uint8_t* sx = sa + NA * KB * TW_SUB;
-    float* sp = (float*)(sx + NA * KB * XSUB);  // [token][row] sums of a finished tile
+    uint8_t* sx = sa + NA * TW_SUB;
+    float* sp = (float*)(sx + NA * XSUB);  // [token][row] sums of a finished tile
     uint8_t* sw = (uint8_t*)sp + NTOK * TW_ROWS * 4;
     uint64_t* bars = (uint64_t*)(sw + NW * WST);
     uint32_t* s_tmem = (uint32_t*)(bars + 40);
@@ -150,17 +162,17 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
     const uint32_t wfull = smem_u32(bars), wempty = wfull + 8 * NW, xfull = wempty + 8 * NW,
                    afull = xfull + 8 * NA, aempty = afull + 8 * NA, tfull = aempty + 8 * NA,
                    tempty = tfull + 16, mdone = tempty + 16, pready = mdone + 8,
-                   pfree = pready + 8;  // aempty frees the X stage too: one commit covers both
+                   pfree = pready + 8;  // aempty frees the x chunk too: one commit covers both
     static_assert(2 * NW + 3 * NA + 7 <= 40, "barriers");
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NW; ++i) {
             mbar_init(wfull + 8 * i, 1);
-            mbar_init(wempty + 8 * i, TW_DEQ + TW_SUM);
+            mbar_init(wempty + 8 * i, TW_DEQ / 2 * KB + TW_SUM);
         }
         for (int i = 0; i < NA; ++i) {
             mbar_init(xfull + 8 * i, 1);
-            mbar_init(afull + 8 * i, TW_DEQ);
+            mbar_init(afull + 8 * i, TW_DEQ / 2);
             mbar_init(aempty + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -186,19 +198,19 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
 
-    if (warp == 0) {
-        if (lane == 0) {
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if (warp == 0 && lane == 0) {
             // ---------------- producer
-            int i = 0;
+            int i = 0, ci = 0;
             bool ok = true;
             for (int64_t tile = cl; tile < a.tiles && ok; tile += a.C) {
                 const int64_t rt = tile / a.tt, u0 = rt * 4;
                 const int tok0 = (int)(tile - rt * a.tt) * NTOK;
                 const int nu = (int)min((int64_t)4, a.units - u0);
-                for (int s = 0; s < nst; ++s, ++i) {
-                    const int w = i % NW, x = i % NA;
-                    if ((i >= NW && !mbar_wait(wempty + 8 * w, (i / NW - 1) & 1)) ||
-                        (i >= NA && !mbar_wait(aempty + 8 * x, (i / NA - 1) & 1))) {
+                for (int s = 0; s < nst && ok; ++s, ++i) {
+                    const int w = i % NW;
+                    if (i >= NW && !mbar_wait(wempty + 8 * w, (i / NW - 1) & 1)) {
                         atomicOr(&g_dev_err, ERR_PRODUCER);
                         ok = false;
                         break;
@@ -208,121 +220,148 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
                         bulk_g2s_nx(smem_u32(sw + w * WST + u * STEP),
                                     a.packed + ((u0 + u) * a.steps + k0 + s) * STEP, STEP,
                                     wfull + 8 * w);
-                    mbar_expect_tx(xfull + 8 * x, (uint32_t)(KB * XSUB));
 #pragma unroll
-                    for (int c = 0; c < KB; ++c)
-                        tw_load_x(smem_u32(sx + (x * KB + c) * XSUB), &map_x,
-                                  ((k0 + s) * KB + c) * W4_CHUNK, tok0, xfull + 8 * x);
+                    for (int c = 0; c < KB; ++c, ++ci) {
+                        const int x = ci % NA;
+                        if (ok && ci >= NA && !mbar_wait(aempty + 8 * x, (ci / NA - 1) & 1)) {
+                            atomicOr(&g_dev_err, ERR_PRODUCER);
+                            ok = false;
+                        }
+                        if (!ok) break;
+                        mbar_expect_tx(xfull + 8 * x, (uint32_t)XSUB);
+                        tw_load_x(smem_u32(sx + x * XSUB), &map_x, ((k0 + s) * KB + c) * W4_CHUNK, tok0,
+                                  xfull + 8 * x);
+                    }
+                    if (!ok) {  // the step's weights are on their way all the same
+                        ++i;
+                        break;
+                    }
                 }
             }
             // the last copies have landed before the CTA may leave
             for (int q = i > NW ? i - NW : 0; q < i; ++q)
                 if (!mbar_wait(wfull + 8 * (q % NW), (q / NW) & 1)) atomicOr(&g_dev_err, ERR_DRAIN);
-            for (int q = i > NA ? i - NA : 0; q < i; ++q)
+            for (int q = ci > NA ? ci - NA : 0; q < ci; ++q)
                 if (!mbar_wait(xfull + 8 * (q % NA), (q / NA) & 1)) atomicOr(&g_dev_err, ERR_DRAIN);
-        }
-    } else if (warp == 1) {
-        if (lane == 0) {
+        } else if (warp == 1 && lane == 0) {
             // ---------------- MMA issuer
-            int i = 0, j = 0;
+            int ci = 0, j = 0;
             bool ok = true;
             for (int64_t tile = cl; tile < a.tiles && ok; tile += a.C) {
                 const int64_t left = a.tokens - (tile % a.tt) * NTOK;
                 const uint32_t idesc =
                     instr_desc(TW_ROWS, (int)min((int64_t)NTOK, (left + 15) / 16 * 16));
-                for (int s = 0; s < nst && ok; ++s, ++i) {
-                    const int st = i % NA;
-                    if (!mbar_wait(afull + 8 * st, (i / NA) & 1) ||
-                        !mbar_wait(xfull + 8 * st, (i / NA) & 1)) {
-                        atomicOr(&g_dev_err, ERR_MMA);
-                        ok = false;
-                        break;
-                    }
+                for (int s = 0; s < nst && ok; ++s) {
 #pragma unroll
-                    for (int h = 0; h < SG; ++h, ++j) {
-                        const int buf = j & 1;
-                        if (ok && j >= 2 && !mbar_wait(tempty + 8 * buf, ((j - 2) >> 1) & 1)) {
+                    for (int c = 0; c < KB; ++c, ++ci) {
+                        const int st = ci % NA;
+                        if (ok && (!mbar_wait(afull + 8 * st, (ci / NA) & 1) ||
+                                   !mbar_wait(xfull + 8 * st, (ci / NA) & 1))) {
                             atomicOr(&g_dev_err, ERR_MMA);
                             ok = false;
                         }
                         if (!ok) break;
-                        tc_fence_after();
-                        const uint32_t d = tmem + (uint32_t)(buf * NTOK);
-                        constexpr int KK = KB * 4 / SG;  // K = 16 products of a group's part
+                        const uint32_t ao = smem_u32(sa + st * TW_SUB), xo = smem_u32(sx + st * XSUB);
 #pragma unroll
-                        for (int kk = 0; kk < KK; ++kk) {
-                            const int q = h * KK + kk;
-                            const uint32_t ao = smem_u32(sa + (st * KB + (q >> 2)) * TW_SUB) + (q & 3) * 32;
-                            const uint32_t xo = smem_u32(sx + (st * KB + (q >> 2)) * XSUB) + (q & 3) * 32;
-                            mma_bf16(d, smem_desc(ao), smem_desc(xo), idesc, kk > 0 ? 1u : 0u);
+                        for (int kk = 0; kk < 4; ++kk) {
+                            // a group's part of the step starts: every two products, or
+                            // once a step
+                            const bool first = G32 ? kk % 2 == 0 : kk == 0 && c == 0;
+                            const bool last = G32 ? kk % 2 == 1 : kk == 3 && c == KB - 1;
+                            const int buf = j & 1;
+                            if (first) {
+                                if (ok && j >= 2 && !mbar_wait(tempty + 8 * buf, ((j - 2) >> 1) & 1)) {
+                                    atomicOr(&g_dev_err, ERR_MMA);
+                                    ok = false;
+                                }
+                            }
+                            if (!ok) break;
+                            if (first || kk == 0) tc_fence_after();
+                            mma_bf16(tmem + (uint32_t)(buf * NTOK), smem_desc(ao + kk * 32),
+                                     smem_desc(xo + kk * 32), idesc, first ? 0u : 1u);
+                            if (last) {
+                                mma_commit(tfull + 8 * buf);
+                                ++j;
+                            }
                         }
-                        mma_commit(tfull + 8 * buf);
+                        if (!ok) break;
+                        mma_commit(aempty + 8 * st);
                     }
-                    if (ok) mma_commit(aempty + 8 * st);
                 }
             }
             mma_commit(mdone);  // every MMA this thread issued has completed once this fires
         }
-    } else if (warp < 2 + TW_DEQ) {
-        // ---------------- codes to operands: half blocks (16 rows x 64 k) of a step
-        const int d = warp - 2;
+    } else if (warp < 4 + TW_DEQ) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        // ---------------- codes to operands: a warp takes a half block (16 rows x 64 k)
+        // of every other chunk
+        const int d = (warp - 4) & 7, grp = (warp - 4) >> 3;
+        const int u = d >> 1, b = d & 1;
         const int r = lane >> 2, c = lane & 3;
         const bool odd = (r & 1) != 0;  // odd rows store their second half first: the
                                         // eight lanes of a store then hit all banks
-        int i = 0;
+        const int o0 = ((4 * (odd ? 1 : 0) + c) ^ r) * 16, o1 = ((4 * (odd ? 0 : 1) + c) ^ r) * 16;
+        const uint8_t* src0 = sw + u * STEP + b * 512 + lane * 16;
+        const uint8_t* zsrc0 = sw + u * STEP + KB * W4_CHUNK_BYTES + r * LB;
+        uint8_t* dst0 = sa + (u * 32 + b * 16 + r) * 128;
         bool ok = true;
-        for (int64_t tile = cl; tile < a.tiles && ok; tile += a.C) {
-            for (int s = 0; s < nst; ++s, ++i) {
-                const int w = i % NW, st = i % NA;
-                if (!mbar_wait(wfull + 8 * w, (i / NW) & 1) ||
-                    (i >= NA && !mbar_wait(aempty + 8 * st, (i / NA - 1) & 1))) {
-                    if (lane == 0) atomicOr(&g_dev_err, ERR_EPILOGUE);
-                    ok = false;
-                    break;
+        int64_t left = 0;  // chunks of all this CTA's tiles
+        for (int64_t tile = cl; tile < a.tiles; tile += a.C) left += nst * KB;
+        int i = grp / KB, m = grp % KB;  // step and its chunk
+        int w = i % NW, wr = i / NW;
+        for (int64_t ci = grp; ci < left && ok; ci += 2) {
+            const int st = (int)(ci % NA);
+            if (!mbar_wait(wfull + 8 * w, wr & 1) ||
+                (ci >= NA && !mbar_wait(aempty + 8 * st, (int)(ci / NA - 1) & 1))) {
+                if (lane == 0) atomicOr(&g_dev_err, ERR_EPILOGUE);
+                ok = false;
+                break;
+            }
+            const uint4 v = *(const uint4*)(src0 + w * WST + m * W4_CHUNK_BYTES);
+            uint32_t z[2][2];  // [half of the 64 k][row r, r + 8]
+            {
+                W4Scale<FMT> zs;
+                if constexpr (FMT != 0) zs.load(zsrc0 + w * WST);
+                z[0][0] = z[1][0] = b ? zs.zero2(2) : zs.zero2(0);
+                z[0][1] = z[1][1] = b ? zs.zero2(3) : zs.zero2(1);
+                if constexpr (G32 && FMT != 0) {
+                    zs.load(zsrc0 + w * WST + SB);
+                    z[1][0] = b ? zs.zero2(2) : zs.zero2(0);
+                    z[1][1] = b ? zs.zero2(3) : zs.zero2(1);
                 }
+            }
+            uint8_t* dst = dst0 + st * TW_SUB;
 #pragma unroll
-                for (int m = 0; m < KB; ++m) {
-                    // of the step's 8 KB half blocks: unit u, half b, chunk m
-                    const int u = d >> 1, b = d & 1;
-                    const uint8_t* blk = sw + w * WST + u * STEP;
-                    const uint4 v = *(const uint4*)(blk + m * W4_CHUNK_BYTES + b * 512 + lane * 16);
-                    W4Scale<FMT> zs[SG];
-                    if constexpr (FMT != 0) {
-#pragma unroll
-                        for (int h = 0; h < SG; ++h) zs[h].load(blk + KB * W4_CHUNK_BYTES + h * SB + r * LB);
-                    }
-                    uint8_t* dst = sa + (st * KB + m) * TW_SUB + (u * 32 + b * 16 + r) * 128;
-#pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        const bool second = odd != (hh == 1);  // which half of the row's 64 k
-                        const int off = ((4 * (second ? 1 : 0) + c) ^ r) * 16;
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {  // rows r and r + 8
-                            const uint32_t word = q == 0 ? (second ? v.y : v.x) : (second ? v.w : v.z);
-                            uint32_t zz = zs[0].zero2(2 * b + q);
-                            if constexpr (G32 && FMT != 0) {
-                                const uint32_t z1 = zs[SG - 1].zero2(2 * b + q);
-                                zz = second ? z1 : zz;
-                            }
-                            *(uint4*)(dst + q * 1024 + off) =
-                                make_uint4(w4_pair_exact(word, 0, zz), w4_pair_exact(word, 1, zz),
-                                           w4_pair_exact(word, 2, zz), w4_pair_exact(word, 3, zz));
-                        }
-                    }
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(afull + 8 * st);
-                    mbar_arrive(wempty + 8 * w);
-                }
+            for (int q = 0; q < 2; ++q) {
+                const uint32_t wa = q == 0 ? (odd ? v.y : v.x) : (odd ? v.w : v.z);
+                const uint32_t wb = q == 0 ? (odd ? v.x : v.y) : (odd ? v.z : v.w);
+                const uint32_t za = odd ? z[1][q] : z[0][q], zb = odd ? z[0][q] : z[1][q];
+                *(uint4*)(dst + q * 1024 + o0) =
+                    make_uint4(w4_pair_exact(wa, 0, za), w4_pair_exact(wa, 1, za),
+                               w4_pair_exact(wa, 2, za), w4_pair_exact(wa, 3, za));
+                *(uint4*)(dst + q * 1024 + o1) =
+                    make_uint4(w4_pair_exact(wb, 0, zb), w4_pair_exact(wb, 1, zb),
+                               w4_pair_exact(wb, 2, zb), w4_pair_exact(wb, 3, zb));
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(afull + 8 * st);
+                mbar_arrive(wempty + 8 * w);
+            }
+            if constexpr (KB == 2) {
+                if (++w == NW) w = 0, ++wr;
+            } else {
+                w += 2;
+                if (w >= NW) w -= NW, ++wr;
             }
         }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
         // ---------------- scaling and sums
         const int q = warp & 3;                     // TMEM lanes 32 q .. 32 q + 31 = unit q
-        const int half = (warp - 2 - TW_DEQ) >> 2;  // columns half * NC ..
-        const int e = threadIdx.x - 32 * (2 + TW_DEQ);
+        const int half = (warp - 4 - TW_DEQ) >> 2;  // columns half * NC ..
+        const int e = threadIdx.x - 32 * (4 + TW_DEQ);
         const uint32_t tb = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(half * NC);
         const int srow = (lane & 7) * LB, sj = lane >> 3;  // this row's scale
         int i = 0, j = 0, ntile = 0;
@@ -357,15 +396,20 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t ta = tb + (uint32_t)(buf * NTOK);
+                    constexpr int G = NC >= 32 ? 2 : 1;  // 16-column loads in flight
 #pragma unroll
-                    for (int n = 0; n < NC; n += 16) {
+                    for (int n = 0; n < NC; n += 16 * G) {
                         if (half * NC + n < ntok) {  // the same for the whole warp
-                            uint32_t v[16];
-                            tmem_ld16(ta + n, v);
+                            uint32_t v[G][16];
+#pragma unroll
+                            for (int g = 0; g < G; ++g) tmem_ld(ta + n + 16 * g, v[g]);
                             asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-                            for (int z = 0; z < 16; ++z)
-                                acc[n + z] = fmaf(sc[h], __uint_as_float(v[z]), acc[n + z]);
+                            for (int g = 0; g < G; ++g)
+#pragma unroll
+                                for (int z = 0; z < 16; ++z)
+                                    acc[n + 16 * g + z] =
+                                        fmaf(sc[h], __uint_as_float(v[g][z]), acc[n + 16 * g + z]);
                         }
                     }
                     tc_fence_before();
@@ -395,40 +439,75 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
             }
             // this CTA writes its share of the tokens
             const int t0 = NTOK * rank / a.S, t1 = min(NTOK * (rank + 1) / a.S, ntok);
+            // four rows of a token at a time, four such items in flight
             const uint32_t spu = smem_u32(sp);
-            auto sum_at = [&](int row, int t) {
-                const int o = t * TW_ROWS + row;
-                if (a.S == 1) return sp[o];
-                float v = 0.0f;
-                for (int k = 0; k < a.S; ++k) v += ld_cluster(spu + 4 * o, k);
-                return v;
+            auto sum4 = [&](int row, int t, float (&v)[4]) {
+                const uint32_t o = spu + 4 * (t * TW_ROWS + row);
+                v[0] = v[1] = v[2] = v[3] = 0.0f;
+                for (int k = 0; k < a.S; ++k) {
+                    const float4 f = ld_cluster4(o, k);
+                    v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
+                }
             };
-            if (ok) {
-                if (!a.x_prev) {
-                    const int64_t n = rt * TW_ROWS + (e & 127);
-                    if (n < a.n_rows)
-                        for (int t = t0 + (e >> 7); t < t1; t += 2) {
-                            const float v = sum_at(e & 127, t);
-                            const int64_t o = (tok0 + t) * a.ld + n;
+            if (ok && !a.x_prev) {
+                const int row = (e & 31) * 4;
+                const int64_t n = rt * TW_ROWS + row;
+                for (int t = t0 + (e >> 5); t < t1; t += 32) {
+                    float v[4][4];
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) sum4(row, min(t + 8 * z, t1 - 1), v[z]);
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        if (t + 8 * z >= t1) break;
+                        const int64_t o = (tok0 + t + 8 * z) * a.ld + n;
+                        if (a.y_vec && n + 4 <= a.n_rows) {
                             if (a.y_bf16)
-                                ((__nv_bfloat16*)a.y)[o] = __float2bfloat16_rn(v);
+                                *(uint2*)((__nv_bfloat16*)a.y + o) = pack4(v[z]);
                             else
-                                ((float*)a.y)[o] = v;
+                                *(float4*)((float*)a.y + o) = make_float4(v[z][0], v[z][1], v[z][2], v[z][3]);
+                        } else {
+#pragma unroll
+                            for (int p = 0; p < 4; ++p)
+                                if (n + p < a.n_rows) {
+                                    if (a.y_bf16)
+                                        ((__nv_bfloat16*)a.y)[o + p] = __float2bfloat16_rn(v[z][p]);
+                                    else
+                                        ((float*)a.y)[o + p] = v[z][p];
+                                }
                         }
-                } else {
-                    // a and b of a channel: rows 8 apart (w4_pack, taps)
-                    const int cl64 = e & 63, row = (cl64 >> 3) * 16 + (cl64 & 7);
-                    const int64_t ch = rt * 64 + cl64;
-                    if (ch < a.ld)
-                        for (int t = t0 + (e >> 6); t < t1; t += 4) {
-                            const int64_t tok = tok0 + t;
-                            const float av = sum_at(row, t), bv = sum_at(row + 8, t);
-                            const float xc = __bfloat162float(a.x[tok * a.ld + ch]);
-                            const float xp = __bfloat162float(
-                                tok % a.T == 0 ? a.x_prev[tok / a.T * a.ld + ch] : a.x[(tok - 1) * a.ld + ch]);
-                            ((__nv_bfloat16*)a.y)[tok * a.ld + ch] =
-                                __float2bfloat16_rn(fmaf(bv, xp, fmaf(av, xc, xc)));
-                        }
+                    }
+                }
+            } else if (ok) {
+                // a and b of a channel: rows 8 apart (w4_pack, taps); H is a multiple
+                // of 64, so a tile's 64 channels are all there
+                const int c4 = (e & 15) * 4, row = (c4 >> 3) * 16 + (c4 & 7);
+                const int64_t ch = rt * 64 + c4;
+                for (int t = t0 + (e >> 4); t < t1; t += 32) {
+                    float av[2][4], bv[2][4];
+                    uint2 xc[2], xp[2];
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        const int64_t tok = tok0 + min(t + 16 * z, t1 - 1);
+                        xc[z] = *(const uint2*)(a.x + tok * a.ld + ch);
+                        xp[z] = *(const uint2*)(tok % a.T == 0 ? a.x_prev + tok / a.T * a.ld + ch
+                                                               : a.x + (tok - 1) * a.ld + ch);
+                    }
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        sum4(row, min(t + 16 * z, t1 - 1), av[z]);
+                        sum4(row + 8, min(t + 16 * z, t1 - 1), bv[z]);
+                    }
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        if (t + 16 * z >= t1) break;
+                        float c[4], p[4];
+                        unpack4(xc[z], c);
+                        unpack4(xp[z], p);
+#pragma unroll
+                        for (int q2 = 0; q2 < 4; ++q2)
+                            c[q2] = fmaf(bv[z][q2], p[q2], fmaf(av[z][q2], c[q2], c[q2]));
+                        *(uint2*)((__nv_bfloat16*)a.y + (tok0 + t + 16 * z) * a.ld + ch) = pack4(c);
+                    }
                 }
             }
             asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -532,6 +611,7 @@ int dfl_linear_w4_tc(const W4Call& c, const W4Dev& d, cudaStream_t s) {
     a.tiles = (L.units + 3) / 4 * a.tt;
     a.y = c.y;
     a.y_bf16 = c.y_bf16;
+    a.y_vec = L.N % 4 == 0 && (uintptr_t)c.y % 16 == 0;
     a.x = (const __nv_bfloat16*)c.x;
     a.x_prev = (const __nv_bfloat16*)c.x_prev;
     a.T = c.T;

@@ -24,21 +24,20 @@
 // entries in the order (r mod 8, r / 8), so the four rows a lane works on are
 // adjacent:
 //   format 0 (bf16 scales, zero = 8): 4 bf16 per lane-row, 64 bytes a group
-//   DFLASH2_W4_ZERO:                  4 bf16 + 4 bf16 of (128 + zero), 128 bytes
-//   DFLASH2_W4_SCALE_F32:             4 float + 4 bf16 of (128 + zero) + 8 pad, 256 bytes
+//   DFLASH2_W4_ZERO:                  4 bf16 + 4 bf16 of (16 + zero), 128 bytes
+//   DFLASH2_W4_SCALE_F32:             4 float + 4 bf16 of (16 + zero) + 8 pad, 256 bytes
 // Rows past N have scale 0; the K tail of a last half chunk has codes equal
 // to its zero point and, where it is a group of its own, scale 0.
 //
-// Codes to operands, two ways:
-//   - exact: 0x4300 | q is the bf16 value 128 + q; subtracting (128 + zero)
-//     leaves q - zero, an integer of at most 8 bits, exactly.  The products with
-//     x then accumulate in fp32 with no rounding of the weights, and the group's
-//     scale multiplies the fp32 sum.
-//   - offset: 0x4180 | q << 3 is 16 + q, with no subtraction, and the sum starts
-//     at -(16 + zero) * sum of x instead of zero.  A third fewer instructions,
-//     but the fp32 sum passes through magnitudes a few times those of the
-//     result, and its last bits go with them (about 2e-6 of the result): it
-//     serves bf16 outputs, whose own rounding is a thousand times that.
+// Codes to operands: 0x4180 | q << 3 is the bf16 value 16 + q.
+//   - exact: subtracting (16 + zero) leaves q - zero, an integer below 16 in
+//     magnitude, exactly.  The products with x then accumulate in fp32 with no
+//     rounding of the weights, and the group's scale multiplies the fp32 sum.
+//   - offset: no subtraction; the sum starts at -(16 + zero) * sum of x instead of
+//     zero.  A third fewer instructions, but the fp32 sum passes through
+//     magnitudes a few times those of the result, and its last bits go with them
+//     (about 2e-6 of the result): it serves bf16 outputs, whose own rounding is a
+//     thousand times that.
 #pragma once
 
 #include "common.cuh"
@@ -95,17 +94,16 @@ __device__ __forceinline__ uint32_t w4_and_or(uint32_t w, uint32_t mask, uint32_
     asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(t) : "r"(w), "r"(mask), "r"(magic));
     return t;
 }
-// The pair (2 j, 2 j + 1) of a word as bf16x2, minus the zero points; zz =
-// bf16x2 of (128 + zero) twice.
+// The pair (2 j, 2 j + 1) of a word as bf16x2, plus 16 (zero points left in) ...
+__device__ __forceinline__ uint32_t w4_pair_offset(uint32_t w, int j) {
+    return w4_and_or(w4_turn(w, 4 * j), 0x00780078u, 0x41804180u);
+}
+// ... and minus the zero points; zz = bf16x2 of (16 + zero) twice.
 __device__ __forceinline__ uint32_t w4_pair_exact(uint32_t w, int j, uint32_t zz) {
-    const uint32_t t = w4_and_or(w4_turn(w, 3 + 4 * j), 0x000F000Fu, 0x43004300u);
+    const uint32_t t = w4_pair_offset(w, j);
     __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&t),
                                *reinterpret_cast<const __nv_bfloat162*>(&zz));
     return *reinterpret_cast<uint32_t*>(&d);
-}
-// The same plus 16, zero points left in.
-__device__ __forceinline__ uint32_t w4_pair_offset(uint32_t w, int j) {
-    return w4_and_or(w4_turn(w, 4 * j), 0x00780078u, 0x41804180u);
 }
 
 // The scales (and zero points) of the four rows r, r + 8, r + 16, r + 24 of a
@@ -134,7 +132,7 @@ struct W4Scale {
         return __uint_as_float((i & 1) ? (raw[i >> 1] & 0xFFFF0000u) : (raw[i >> 1] << 16));
     }
     __device__ __forceinline__ uint32_t zero2(int i) const {
-        if constexpr (FMT == 0) return 0x43084308u;  // 128 + 8
+        if constexpr (FMT == 0) return 0x41C041C0u;  // 16 + 8
         const uint32_t w = raw[((FMT & DFLASH2_W4_SCALE_F32) ? 4 : 2) + (i >> 1)];
         return (i & 1) ? __byte_perm(w, 0, 0x3232) : __byte_perm(w, 0, 0x1010);
     }
@@ -142,7 +140,7 @@ struct W4Scale {
     __device__ __forceinline__ float zero16(int i) const {
         if constexpr (FMT == 0) return 24.0f;
         const uint32_t w = raw[((FMT & DFLASH2_W4_SCALE_F32) ? 4 : 2) + (i >> 1)];
-        return __uint_as_float((i & 1) ? (w & 0xFFFF0000u) : (w << 16)) - 112.0f;
+        return __uint_as_float((i & 1) ? (w & 0xFFFF0000u) : (w << 16));
     }
 };
 
