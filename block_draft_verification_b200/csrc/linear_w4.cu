@@ -192,6 +192,7 @@ __global__ void __launch_bounds__(W4_THREADS, 1) linear_w4_kernel(const W4Args a
     // The run at hand, of batch ub and phase ph: its items are cu, cc (unit and
     // step) onward; `left` of them are not yet requested.
     int c0 = 0, nc = 0, n = 0, cu = 0, cc = 0, len = 0, left = 0, lc = 0, st_load = 0, st_read = 0;
+    int64_t lu = 0;  // unit and step (of the run's part of K) of the next request
     const uint8_t* lw = nullptr;
     auto request = [&]() {  // the next step into the ring (an empty group at the run's end)
         if (left > 0) {
@@ -213,10 +214,10 @@ __global__ void __launch_bounds__(W4_THREADS, 1) linear_w4_kernel(const W4Args a
                 }
             }
             st_load = st_load + 1 == D ? 0 : st_load + 1;
-            lw += STEP;
+            lw += 4 * STEP;
             if (++lc == nc) {
                 lc = 0;
-                lw += (int64_t)(a.steps - nc) * STEP;
+                lw = a.packed + w4_block(++lu, a.steps, c0, STEP);
             }
         }
         cp_async_commit();
@@ -232,7 +233,8 @@ __global__ void __launch_bounds__(W4_THREADS, 1) linear_w4_kernel(const W4Args a
         left = len = i1 - i0;
         cu = nc > 0 ? i0 / nc : 0;
         lc = cc = i0 - cu * nc;
-        lw = a.packed + ((ub + cu) * a.steps + c0 + cc) * STEP;
+        lu = ub + cu;
+        lw = a.packed + w4_block(lu, a.steps, c0 + cc, STEP);
         st_load = st_read = 0;
 #pragma unroll
         for (int d = 0; d < D - 1; ++d) request();
@@ -483,15 +485,15 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const uint8_t* __restrict_
         if (z > 15u) atomicOr(&g_dev_err, (unsigned)ERR_INPUT);
         return min(z, 15u);
     };
-    const int64_t blocks = L.units * L.steps;
+    const int64_t blocks = (L.units + 3) / 4 * 4 * L.steps;
     const int vecs = L.kb * (W4_CHUNK_BYTES / 16);  // per block
     const int64_t nv = blocks * vecs, ns = blocks * L.sg * W4_UNIT;
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < nv + ns;
          i += (int64_t)gridDim.x * blockDim.x) {
         if (i < nv) {
-            const int64_t blk = i / vecs, u = blk / L.steps;
+            const int64_t blk = i / vecs, u = (blk >> 2) / L.steps * 4 + (blk & 3);
             const int v = (int)(i - blk * vecs), b = (v >> 5) & 1, lane = v & 31;
-            const int64_t c = (blk - u * L.steps) * L.kb + (v >> 6);
+            const int64_t c = (blk >> 2) % L.steps * L.kb + (v >> 6);
             uint32_t w[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {  // row r or r + 8, half h
@@ -512,10 +514,10 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const uint8_t* __restrict_
         } else {
             const int64_t e = i - nv;
             const int j = (int)(e & 3), g8 = (int)((e >> 2) & 7);  // row = 8 j + g8
-            const int64_t bg = e >> 5, blk = bg / L.sg, u = blk / L.steps;
+            const int64_t bg = e >> 5, blk = bg / L.sg, u = (blk >> 2) / L.steps * 4 + (blk & 3);
             const int h = (int)(bg - blk * L.sg);
             const int64_t row = u * W4_UNIT + 8 * j + g8;
-            const int64_t g = ((blk - u * L.steps) * L.kb * W4_CHUNK + 32 * h) / L.group;
+            const int64_t g = ((blk >> 2) % L.steps * L.kb * W4_CHUNK + 32 * h) / L.group;
             const bool in = row < L.N && g < kg;
             const int64_t src = in ? source(row) * kg + g : 0;
             uint8_t* dst = packed + blk * L.step_bytes + L.kb * W4_CHUNK_BYTES + h * sbytes +
@@ -758,7 +760,7 @@ extern "C" int dflash2_w4_pack(const uint8_t* q, const void* scale, const uint8_
         !aligned(packed, 256))
         return DFLASH2_EALIGN;
     const W4Layout L = w4_layout(N, K, group, format);
-    const int64_t n = L.units * L.steps * (L.kb * (W4_CHUNK_BYTES / 16) + L.sg * W4_UNIT);
+    const int64_t n = (int64_t)(L.total / L.step_bytes) * (L.kb * (W4_CHUNK_BYTES / 16) + L.sg * W4_UNIT);
     const unsigned blocks = (unsigned)std::min<int64_t>((n + 255) / 256, 148 * 32);
     w4_pack_kernel<<<blocks, 256, 0, (cudaStream_t)stream>>>(q, scale, zero, L, format,
                                                              (uint8_t*)packed);

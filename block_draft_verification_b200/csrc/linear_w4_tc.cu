@@ -2,9 +2,9 @@
 // the tensor cores (tcgen05): bf16 activations, any output type.
 //
 // A tile is 128 weight rows (four units) by up to 128 tokens.  Its K loop:
-//   warp 0       bulk copies of the four units' packed steps (64 or 128 k) into the
-//                W ring, TMA of the tokens' x (64 k boxes, 128-byte swizzle) into
-//                the X ring
+//   warp 0       one bulk copy per packed step (64 or 128 k) of the tile into the W
+//                ring
+//   warp 2       TMA of the tokens' x (64 k boxes, 128-byte swizzle) into the X ring
 //   warps 4-19   codes to exact bf16 integers q - zero, stored as the K-major,
 //                128-byte swizzled A tile of a 64 k chunk; the two halves of these
 //                warps take chunks in turn
@@ -201,46 +201,42 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 0 && lane == 0) {
-            // ---------------- producer
-            int i = 0, ci = 0;
+            // ---------------- packed weights
+            int i = 0;
             bool ok = true;
             for (int64_t tile = cl; tile < a.tiles && ok; tile += a.C) {
-                const int64_t rt = tile / a.tt, u0 = rt * 4;
-                const int tok0 = (int)(tile - rt * a.tt) * NTOK;
-                const int nu = (int)min((int64_t)4, a.units - u0);
-                for (int s = 0; s < nst && ok; ++s, ++i) {
+                const uint8_t* src = a.packed + w4_block(tile / a.tt * 4, a.steps, k0, STEP);
+                for (int s = 0; s < nst; ++s, ++i, src += WST) {
                     const int w = i % NW;
                     if (i >= NW && !mbar_wait(wempty + 8 * w, (i / NW - 1) & 1)) {
                         atomicOr(&g_dev_err, ERR_PRODUCER);
                         ok = false;
                         break;
                     }
-                    mbar_expect_tx(wfull + 8 * w, (uint32_t)(nu * STEP));
-                    for (int u = 0; u < nu; ++u)
-                        bulk_g2s_nx(smem_u32(sw + w * WST + u * STEP),
-                                    a.packed + ((u0 + u) * a.steps + k0 + s) * STEP, STEP,
-                                    wfull + 8 * w);
-#pragma unroll
-                    for (int c = 0; c < KB; ++c, ++ci) {
-                        const int x = ci % NA;
-                        if (ok && ci >= NA && !mbar_wait(aempty + 8 * x, (ci / NA - 1) & 1)) {
-                            atomicOr(&g_dev_err, ERR_PRODUCER);
-                            ok = false;
-                        }
-                        if (!ok) break;
-                        mbar_expect_tx(xfull + 8 * x, (uint32_t)XSUB);
-                        tw_load_x(smem_u32(sx + x * XSUB), &map_x, ((k0 + s) * KB + c) * W4_CHUNK, tok0,
-                                  xfull + 8 * x);
-                    }
-                    if (!ok) {  // the step's weights are on their way all the same
-                        ++i;
-                        break;
-                    }
+                    bulk_g2s(smem_u32(sw + w * WST), src, WST, wfull + 8 * w);
                 }
             }
             // the last copies have landed before the CTA may leave
             for (int q = i > NW ? i - NW : 0; q < i; ++q)
                 if (!mbar_wait(wfull + 8 * (q % NW), (q / NW) & 1)) atomicOr(&g_dev_err, ERR_DRAIN);
+        } else if (warp == 2 && lane == 0) {
+            // ---------------- x
+            int ci = 0;
+            bool ok = true;
+            for (int64_t tile = cl; tile < a.tiles && ok; tile += a.C) {
+                const int tok0 = (int)(tile % a.tt) * NTOK;
+                for (int s = 0; s < nst * KB; ++s, ++ci) {
+                    const int x = ci % NA;
+                    if (ci >= NA && !mbar_wait(aempty + 8 * x, (ci / NA - 1) & 1)) {
+                        atomicOr(&g_dev_err, ERR_PRODUCER);
+                        ok = false;
+                        break;
+                    }
+                    mbar_expect_tx(xfull + 8 * x, (uint32_t)XSUB);
+                    tw_load_x(smem_u32(sx + x * XSUB), &map_x, (k0 * KB + s) * W4_CHUNK, tok0,
+                              xfull + 8 * x);
+                }
+            }
             for (int q = ci > NA ? ci - NA : 0; q < ci; ++q)
                 if (!mbar_wait(xfull + 8 * (q % NA), (q / NA) & 1)) atomicOr(&g_dev_err, ERR_DRAIN);
         } else if (warp == 1 && lane == 0) {
@@ -301,33 +297,35 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
         const bool odd = (r & 1) != 0;  // odd rows store their second half first: the
                                         // eight lanes of a store then hit all banks
         const int o0 = ((4 * (odd ? 1 : 0) + c) ^ r) * 16, o1 = ((4 * (odd ? 0 : 1) + c) ^ r) * 16;
-        const uint8_t* src0 = sw + u * STEP + b * 512 + lane * 16;
-        const uint8_t* zsrc0 = sw + u * STEP + KB * W4_CHUNK_BYTES + r * LB;
+        const uint8_t* src = sw + u * STEP + b * 512 + lane * 16;
+        // the zero points of rows r and r + 8 of this half
+        const uint8_t* zsrc = sw + u * STEP + KB * W4_CHUNK_BYTES + r * LB +
+                              ((FMT & DFLASH2_W4_SCALE_F32) ? 16 : 8) + 4 * b;
         uint8_t* dst0 = sa + (u * 32 + b * 16 + r) * 128;
-        bool ok = true;
-        int64_t left = 0;  // chunks of all this CTA's tiles
+        int left = 0;  // chunks of this CTA's tiles that this half of the warps takes
         for (int64_t tile = cl; tile < a.tiles; tile += a.C) left += nst * KB;
-        int i = grp / KB, m = grp % KB;  // step and its chunk
-        int w = i % NW, wr = i / NW;
-        for (int64_t ci = grp; ci < left && ok; ci += 2) {
-            const int st = (int)(ci % NA);
-            if (!mbar_wait(wfull + 8 * w, wr & 1) ||
-                (ci >= NA && !mbar_wait(aempty + 8 * st, (int)(ci / NA - 1) & 1))) {
+        left = (left - grp + 1) / 2;
+        int w = KB == 2 ? 0 : grp % NW;
+        uint32_t wpar = 0;
+        for (int k = 0; k < left; ++k) {
+            const int st = grp + 2 * (k & 1);  // chunk 2 k + grp, stage by its number mod 4
+            static_assert(NA == 4, "two stages for either half");
+            if (!mbar_wait(wfull + 8 * w, wpar) ||
+                (k >= 2 && !mbar_wait(aempty + 8 * st, ((k >> 1) - 1) & 1))) {
                 if (lane == 0) atomicOr(&g_dev_err, ERR_EPILOGUE);
-                ok = false;
                 break;
             }
-            const uint4 v = *(const uint4*)(src0 + w * WST + m * W4_CHUNK_BYTES);
+            const uint4 v = *(const uint4*)(src + w * WST + (KB == 2 ? grp * W4_CHUNK_BYTES : 0));
             uint32_t z[2][2];  // [half of the 64 k][row r, r + 8]
-            {
-                W4Scale<FMT> zs;
-                if constexpr (FMT != 0) zs.load(zsrc0 + w * WST);
-                z[0][0] = z[1][0] = b ? zs.zero2(2) : zs.zero2(0);
-                z[0][1] = z[1][1] = b ? zs.zero2(3) : zs.zero2(1);
-                if constexpr (G32 && FMT != 0) {
-                    zs.load(zsrc0 + w * WST + SB);
-                    z[1][0] = b ? zs.zero2(2) : zs.zero2(0);
-                    z[1][1] = b ? zs.zero2(3) : zs.zero2(1);
+            z[0][0] = z[0][1] = z[1][0] = z[1][1] = 0x41C041C0u;  // 16 + 8
+            if constexpr (FMT != 0) {
+                const uint32_t q = *(const uint32_t*)(zsrc + w * WST);
+                z[0][0] = z[1][0] = __byte_perm(q, 0, 0x1010);
+                z[0][1] = z[1][1] = __byte_perm(q, 0, 0x3232);
+                if constexpr (G32) {
+                    const uint32_t q1 = *(const uint32_t*)(zsrc + w * WST + SB);
+                    z[1][0] = __byte_perm(q1, 0, 0x1010);
+                    z[1][1] = __byte_perm(q1, 0, 0x3232);
                 }
             }
             uint8_t* dst = dst0 + st * TW_SUB;
@@ -335,7 +333,7 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
             for (int q = 0; q < 2; ++q) {
                 const uint32_t wa = q == 0 ? (odd ? v.y : v.x) : (odd ? v.w : v.z);
                 const uint32_t wb = q == 0 ? (odd ? v.x : v.y) : (odd ? v.z : v.w);
-                const uint32_t za = odd ? z[1][q] : z[0][q], zb = odd ? z[0][q] : z[1][q];
+                const uint32_t za = G32 && odd ? z[1][q] : z[0][q], zb = G32 && odd ? z[0][q] : z[1][q];
                 *(uint4*)(dst + q * 1024 + o0) =
                     make_uint4(w4_pair_exact(wa, 0, za), w4_pair_exact(wa, 1, za),
                                w4_pair_exact(wa, 2, za), w4_pair_exact(wa, 3, za));
@@ -349,11 +347,10 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
                 mbar_arrive(afull + 8 * st);
                 mbar_arrive(wempty + 8 * w);
             }
-            if constexpr (KB == 2) {
-                if (++w == NW) w = 0, ++wr;
-            } else {
-                w += 2;
-                if (w >= NW) w -= NW, ++wr;
+            w += KB == 2 ? 1 : 2;
+            if (w >= NW) {
+                w -= NW;
+                wpar ^= 1u;
             }
         }
     } else {
@@ -370,9 +367,9 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
             const int64_t rt = tile / a.tt;
             const int64_t tok0 = (tile - rt * a.tt) * NTOK;
             const int ntok = (int)min((int64_t)NTOK, a.tokens - tok0);
-            float acc[NC];
+            uint64_t acc[NC / 2];  // pairs of tokens
 #pragma unroll
-            for (int n = 0; n < NC; ++n) acc[n] = 0.0f;
+            for (int n = 0; n < NC / 2; ++n) acc[n] = 0;
             for (int s = 0; s < nst && ok; ++s, ++i) {
                 const int w = i % NW;
                 float sc[SG];
@@ -407,9 +404,11 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
 #pragma unroll
                             for (int g = 0; g < G; ++g)
 #pragma unroll
-                                for (int z = 0; z < 16; ++z)
-                                    acc[n + 16 * g + z] =
-                                        fmaf(sc[h], __uint_as_float(v[g][z]), acc[n + 16 * g + z]);
+                                for (int z = 0; z < 16; z += 2) {
+                                    uint64_t& p = acc[(n + 16 * g + z) / 2];
+                                    p = f2_fma(f2_pack(sc[h], sc[h]),
+                                               f2_pack(__uint_as_float(v[g][z]), __uint_as_float(v[g][z + 1])), p);
+                                }
                         }
                     }
                     tc_fence_before();
@@ -424,8 +423,10 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
                 s_fail[0] = 1;
             } else {
 #pragma unroll
-                for (int n = 0; n < NC; ++n)
-                    sp[(half * NC + n) * TW_ROWS + 32 * q + lane] = acc[n];
+                for (int n = 0; n < NC; n += 2) {
+                    sp[(half * NC + n) * TW_ROWS + 32 * q + lane] = f2_lo(acc[n / 2]);
+                    sp[(half * NC + n + 1) * TW_ROWS + 32 * q + lane] = f2_hi(acc[n / 2]);
+                }
             }
             asm volatile("bar.sync 1, 256;" ::: "memory");
             if (s_fail[0]) break;

@@ -5,9 +5,11 @@
 //
 // Rows are taken in units of 32, K in chunks of 64, and chunks in steps of two
 // where the group is a multiple of 128 (else one).  The packed buffer is one
-// block per unit and step, at (unit * steps + step) * step_bytes: the step's
-// chunks, 1 KB each, then its scales, so that whatever a run of steps needs is
-// contiguous.
+// block per unit and step: the step's chunks, 1 KB each, then its scales.  The
+// blocks of four units follow one another (128 rows of a step are one piece of
+// memory: a bulk copy costs about 60 cycles whatever its size, and 4 KB pieces
+// reach the full rate where 1 KB ones stay below a third), then comes the next
+// step; N is padded to 128 rows.
 //
 // A chunk holds two 16-row halves of 512 bytes, each the operand of four
 // m16n8k16 products: the 16 bytes of lane l are rows r = l / 4 and r + 8, and of
@@ -81,8 +83,12 @@ __host__ __device__ inline W4Layout w4_layout(int64_t N, int64_t K, int group, i
     L.steps = L.chunks / L.kb;
     L.group = group;
     L.step_bytes = L.kb * W4_CHUNK_BYTES + L.sg * w4_scale_bytes(format);
-    L.total = (size_t)L.units * L.steps * L.step_bytes;
+    L.total = (size_t)((L.units + 3) / 4) * L.steps * 4 * L.step_bytes;
     return L;
+}
+// Byte offset of a unit's block of a step.
+__host__ __device__ inline int64_t w4_block(int64_t unit, int steps, int step, int step_bytes) {
+    return (((unit >> 2) * steps + step) * 4 + (unit & 3)) * step_bytes;
 }
 
 __device__ __forceinline__ uint32_t w4_turn(uint32_t w, int bits) {

@@ -24,8 +24,8 @@ def test_packed_bytes(L):
     assert n == 5120 * 5120 // 2 + 5120 * 40 * 2
     assert f(5120, 5120, 128, 1) == 5120 * 5120 // 2 + 5120 * 40 * 4      # zero points beside the scales
     assert f(5120, 5120, 128, 2) == 5120 * 5120 // 2 + 5120 * 40 * 8      # float scales
-    assert f(5119, 5120, 128, 0) == n                                      # rows in units of 32
-    assert f(1, 32, 32, 0) == 1024 + 2 * 64                                # K in chunks of 64
+    assert f(5119, 5120, 128, 0) == n                                      # rows in tiles of 128
+    assert f(1, 32, 32, 0) == 4 * (1024 + 2 * 64)                          # K in chunks of 64
     assert f(2 ** 31 - 1, 2 ** 20, 128, 0) > 2 ** 50                       # 64-bit sizes
     for bad in [(0, 64, 32, 0), (8, 0, 32, 0), (8, 100, 32, 0), (8, 64, 48, 0), (8, 96, 64, 0),
                 (8, 64, 0, 0), (8, 64, -32, 0), (2 ** 31, 64, 32, 0), (8, 2 ** 20 + 64, 64, 0),
