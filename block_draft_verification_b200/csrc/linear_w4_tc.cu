@@ -9,7 +9,7 @@
 //                128-byte swizzled A tile of a 64 k chunk; the two halves of these
 //                warps take chunks in turn
 //   warp 1       tcgen05.mma (M = 128, N = tokens, K = 16) of a group's k into one
-//                of two TMEM accumulators
+//                of four TMEM accumulators
 //   warps 20-27  tcgen05.ld of the group's sums, times the row's scale, added to
 //                fp32 sums in registers while the next group's MMAs run
 // so the weights are never rounded: a group's integer-weighted sums come out of
@@ -120,6 +120,30 @@ __device__ __forceinline__ uint2 pack4(const float (&v)[4]) {
     const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
     return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
+// The MMA warp's instructions, issued by its one elected lane without leaving the
+// warp's common path: operands then stay in the warp's uniform registers (a
+// product takes 15 cycles to issue; about 85 from a branch that one lane takes).
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e;
+}
+__device__ __forceinline__ void mma_bf16_elect(uint32_t elected, uint32_t tmem_d, uint64_t a, uint64_t b,
+                                               uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 e, %5, 0;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(elected));
+}
+__device__ __forceinline__ void mma_commit_elect(uint32_t elected, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(elected)
+        : "memory");
+}
 // 32 lanes x N consecutive fp32 columns, no wait.
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
@@ -143,6 +167,7 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
     constexpr int WST = tw_w_stage(KB, SG, FMT);
     constexpr int XSUB = NTOK * 128;       // bytes of 64 k of x
     constexpr int NC = NTOK / 2;           // columns per summing warp
+    constexpr int NB = 4;                  // accumulators in TMEM
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sa = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t* sx = sa + NA * TW_SUB;
@@ -159,11 +184,11 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
     const int k0 = (int)((int64_t)a.steps * rank / a.S);
     const int nst = (int)((int64_t)a.steps * (rank + 1) / a.S) - k0;
 
-    const uint32_t wfull = smem_u32(bars), wempty = wfull + 8 * NW, xfull = wempty + 8 * NW,
-                   afull = xfull + 8 * NA, aempty = afull + 8 * NA, tfull = aempty + 8 * NA,
-                   tempty = tfull + 16, mdone = tempty + 16, pready = mdone + 8,
-                   pfree = pready + 8;  // aempty frees the x chunk too: one commit covers both
-    static_assert(2 * NW + 3 * NA + 7 <= 40, "barriers");
+    const uint32_t wfull = smem_u32(bars), wempty = wfull + 8 * NW, full = wempty + 8 * NW,
+                   empty = full + 8 * NA, tfull = empty + 8 * NA, tempty = tfull + 8 * NB,
+                   mdone = tempty + 8 * NB, pready = mdone + 8, pfree = pready + 8;
+    // full: a chunk's A tile (one arrival per code warp) and x (one, and its bytes)
+    static_assert(2 * NW + 2 * NA + 2 * NB + 3 <= 40, "barriers");
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NW; ++i) {
@@ -171,11 +196,10 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
             mbar_init(wempty + 8 * i, TW_DEQ / 2 * KB + TW_SUM);
         }
         for (int i = 0; i < NA; ++i) {
-            mbar_init(xfull + 8 * i, 1);
-            mbar_init(afull + 8 * i, TW_DEQ / 2);
-            mbar_init(aempty + 8 * i, 1);
+            mbar_init(full + 8 * i, TW_DEQ / 2 + 1);
+            mbar_init(empty + 8 * i, 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < NB; ++i) {
             mbar_init(tfull + 8 * i, 1);
             mbar_init(tempty + 8 * i, TW_SUM);
         }
@@ -185,7 +209,7 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
         mbar_fence_init();
         s_fail[0] = s_fail[1] = 0;
     }
-    constexpr uint32_t NCOLS = 2 * NTOK;  // two accumulators
+    constexpr uint32_t NCOLS = NB * NTOK;
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(s_tmem)),
@@ -227,21 +251,23 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
                 const int tok0 = (int)(tile % a.tt) * NTOK;
                 for (int s = 0; s < nst * KB; ++s, ++ci) {
                     const int x = ci % NA;
-                    if (ci >= NA && !mbar_wait(aempty + 8 * x, (ci / NA - 1) & 1)) {
+                    if (ci >= NA && !mbar_wait(empty + 8 * x, (ci / NA - 1) & 1)) {
                         atomicOr(&g_dev_err, ERR_PRODUCER);
                         ok = false;
                         break;
                     }
-                    mbar_expect_tx(xfull + 8 * x, (uint32_t)XSUB);
+                    mbar_expect_tx(full + 8 * x, (uint32_t)XSUB);
                     tw_load_x(smem_u32(sx + x * XSUB), &map_x, (k0 * KB + s) * W4_CHUNK, tok0,
-                              xfull + 8 * x);
+                              full + 8 * x);
                 }
             }
             for (int q = ci > NA ? ci - NA : 0; q < ci; ++q)
-                if (!mbar_wait(xfull + 8 * (q % NA), (q / NA) & 1)) atomicOr(&g_dev_err, ERR_DRAIN);
-        } else if (warp == 1 && lane == 0) {
-            // ---------------- MMA issuer
-            int ci = 0, j = 0;
+                if (!mbar_wait(full + 8 * (q % NA), (q / NA) & 1)) atomicOr(&g_dev_err, ERR_DRAIN);
+        } else if (warp == 1) {
+            // ---------------- MMA issuer: the whole warp waits, one lane issues
+            const uint32_t elected = elect_lane();
+            int st = 0, buf = 0;
+            uint32_t par = 0, tpar = 1;  // phases of the operand ring and (waited for) of TMEM
             bool ok = true;
             for (int64_t tile = cl; tile < a.tiles && ok; tile += a.C) {
                 const int64_t left = a.tokens - (tile % a.tt) * NTOK;
@@ -249,43 +275,41 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
                     instr_desc(TW_ROWS, (int)min((int64_t)NTOK, (left + 15) / 16 * 16));
                 for (int s = 0; s < nst && ok; ++s) {
 #pragma unroll
-                    for (int c = 0; c < KB; ++c, ++ci) {
-                        const int st = ci % NA;
-                        if (ok && (!mbar_wait(afull + 8 * st, (ci / NA) & 1) ||
-                                   !mbar_wait(xfull + 8 * st, (ci / NA) & 1))) {
-                            atomicOr(&g_dev_err, ERR_MMA);
-                            ok = false;
-                        }
-                        if (!ok) break;
-                        const uint32_t ao = smem_u32(sa + st * TW_SUB), xo = smem_u32(sx + st * XSUB);
+                    for (int c = 0; c < KB; ++c) {
+                        ok = ok && mbar_wait(full + 8 * st, par);
+                        const uint64_t ao = smem_desc(smem_u32(sa + st * TW_SUB));
+                        const uint64_t xo = smem_desc(smem_u32(sx + st * XSUB));
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
                             // a group's part of the step starts: every two products, or
-                            // once a step
+                            // once a step; its accumulator has been read (its first use:
+                            // the phase before the first counts as done)
                             const bool first = G32 ? kk % 2 == 0 : kk == 0 && c == 0;
                             const bool last = G32 ? kk % 2 == 1 : kk == 3 && c == KB - 1;
-                            const int buf = j & 1;
-                            if (first) {
-                                if (ok && j >= 2 && !mbar_wait(tempty + 8 * buf, ((j - 2) >> 1) & 1)) {
-                                    atomicOr(&g_dev_err, ERR_MMA);
-                                    ok = false;
-                                }
-                            }
+                            if (first) ok = ok && mbar_wait(tempty + 8 * buf, tpar);
                             if (!ok) break;
                             if (first || kk == 0) tc_fence_after();
-                            mma_bf16(tmem + (uint32_t)(buf * NTOK), smem_desc(ao + kk * 32),
-                                     smem_desc(xo + kk * 32), idesc, first ? 0u : 1u);
+                            mma_bf16_elect(elected, tmem + (uint32_t)(buf * NTOK), ao + 2 * kk, xo + 2 * kk,
+                                           idesc, first ? 0u : 1u);
                             if (last) {
-                                mma_commit(tfull + 8 * buf);
-                                ++j;
+                                mma_commit_elect(elected, tfull + 8 * buf);
+                                if (++buf == NB) {
+                                    buf = 0;
+                                    tpar ^= 1u;
+                                }
                             }
                         }
                         if (!ok) break;
-                        mma_commit(aempty + 8 * st);
+                        mma_commit_elect(elected, empty + 8 * st);
+                        if (++st == NA) {
+                            st = 0;
+                            par ^= 1u;
+                        }
                     }
                 }
             }
-            mma_commit(mdone);  // every MMA this thread issued has completed once this fires
+            if (!ok && lane == 0) atomicOr(&g_dev_err, ERR_MMA);
+            mma_commit_elect(elected, mdone);  // fires when every MMA issued has completed
         }
     } else if (warp < 4 + TW_DEQ) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -311,7 +335,7 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
             const int st = grp + 2 * (k & 1);  // chunk 2 k + grp, stage by its number mod 4
             static_assert(NA == 4, "two stages for either half");
             if (!mbar_wait(wfull + 8 * w, wpar) ||
-                (k >= 2 && !mbar_wait(aempty + 8 * st, ((k >> 1) - 1) & 1))) {
+                (k >= 2 && !mbar_wait(empty + 8 * st, ((k >> 1) - 1) & 1))) {
                 if (lane == 0) atomicOr(&g_dev_err, ERR_EPILOGUE);
                 break;
             }
@@ -344,7 +368,7 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(afull + 8 * st);
+                mbar_arrive(full + 8 * st);
                 mbar_arrive(wempty + 8 * w);
             }
             w += KB == 2 ? 1 : 2;
@@ -361,7 +385,8 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
         const int e = threadIdx.x - 32 * (4 + TW_DEQ);
         const uint32_t tb = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(half * NC);
         const int srow = (lane & 7) * LB, sj = lane >> 3;  // this row's scale
-        int i = 0, j = 0, ntile = 0;
+        int w = 0, buf = 0, ntile = 0;
+        uint32_t wpar = 0, tpar = 0;
         bool ok = true;
         for (int64_t tile = cl; tile < a.tiles; tile += a.C, ++ntile) {
             const int64_t rt = tile / a.tt;
@@ -370,10 +395,9 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
             uint64_t acc[NC / 2];  // pairs of tokens
 #pragma unroll
             for (int n = 0; n < NC / 2; ++n) acc[n] = 0;
-            for (int s = 0; s < nst && ok; ++s, ++i) {
-                const int w = i % NW;
+            for (int s = 0; s < nst && ok; ++s) {
                 float sc[SG];
-                ok = mbar_wait(wfull + 8 * w, (i / NW) & 1);
+                ok = mbar_wait(wfull + 8 * w, wpar);
                 if (ok) {
                     const uint8_t* p = sw + w * WST + q * STEP + KB * W4_CHUNK_BYTES + srow;
 #pragma unroll
@@ -385,11 +409,14 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(wempty + 8 * w);
+                    if (++w == NW) {
+                        w = 0;
+                        wpar ^= 1u;
+                    }
                 }
 #pragma unroll
-                for (int h = 0; h < SG; ++h, ++j) {
-                    const int buf = j & 1;
-                    ok = ok && mbar_wait(tfull + 8 * buf, (j >> 1) & 1);
+                for (int h = 0; h < SG; ++h) {
+                    ok = ok && mbar_wait(tfull + 8 * buf, tpar);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t ta = tb + (uint32_t)(buf * NTOK);
@@ -414,6 +441,10 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(tempty + 8 * buf);
+                    if (++buf == NB) {
+                        buf = 0;
+                        tpar ^= 1u;
+                    }
                 }
             }
             // the tile's sums of this CTA's K, then of the cluster's
