@@ -42,8 +42,8 @@ constexpr int TW_DEQ = 16, TW_SUM = 8;  // warps
 constexpr int TW_THREADS = 32 * (4 + TW_DEQ + TW_SUM);
 constexpr int TW_SUB = TW_ROWS * 128;   // bytes of 64 k of A
 constexpr int TW_NA = 4;                // chunks of A, and of x, in their rings
-// Registers: 896 threads are launched with 72 each; 128 x 40 + 512 x 56 + 256 x
-// 112 = 62,464 of the 64,512 are in use after the split.
+// Registers: 896 threads are launched with 72 each, 64,512; 128 x 40 + 512 x 48 +
+// 256 x 136 use all of them after the split.
 
 struct W4TcArgs {
     const uint8_t* packed;
@@ -58,16 +58,26 @@ struct W4TcArgs {
     int T;
 };
 
-// Steps in the W ring.
-__host__ __device__ constexpr int tw_w_stages(int kb) { return kb == 2 ? 3 : 5; }
 __host__ __device__ constexpr int tw_w_stage(int kb, int sg, int fmt) {
     return 4 * (kb * W4_CHUNK_BYTES + sg * w4_scale_bytes(fmt));
 }
-// A ring, X ring, the tile's sums, W ring, barriers, and 1 KB to align the start.
-__host__ __device__ constexpr int tw_smem(int n, int kb, int sg, int fmt) {
-    return 1024 + TW_NA * (TW_SUB + n * 128) + n * TW_ROWS * 4 +
-           tw_w_stages(kb) * tw_w_stage(kb, sg, fmt) + 512;
+// Tokens whose sums are joined at a time at a tile's end.
+__host__ __device__ constexpr int tw_round(int n) { return n < 64 ? n : 64; }
+// Shared memory but for the W ring: 1 KB to align the start, the A and X rings,
+// a round's sums, the barriers.
+__host__ __device__ constexpr int tw_fixed(int n) {
+    return 1024 + TW_NA * (TW_SUB + n * 128) + tw_round(n) * TW_ROWS * 4 + 512;
 }
+// Steps in the W ring: what is left, and no more than 12.
+__host__ __device__ constexpr int tw_w_stages(int n, int kb, int sg, int fmt) {
+    const int w = (227 * 1024 - tw_fixed(n)) / tw_w_stage(kb, sg, fmt);
+    return w < 12 ? w : 12;
+}
+__host__ __device__ constexpr int tw_smem(int n, int kb, int sg, int fmt) {
+    return tw_fixed(n) + tw_w_stages(n, kb, sg, fmt) * tw_w_stage(kb, sg, fmt);
+}
+constexpr int TW_AHEAD = 6;      // steps by which the scales are read before their sums
+constexpr int TW_PREFETCH = 12;  // steps between the request to L2 and the copy
 
 __device__ __forceinline__ void tw_load_x(uint32_t dst, const CUtensorMap* map, int k, int tok,
                                           uint32_t bar) {
@@ -144,6 +154,11 @@ __device__ __forceinline__ void mma_commit_elect(uint32_t elected, uint32_t bar)
         "r"(elected)
         : "memory");
 }
+// The rest of a wait whose barrier was tested earlier (the answer takes about 100
+// cycles, which other work can hide).
+__device__ __forceinline__ bool mbar_settle(bool tried, uint32_t bar, uint32_t parity) {
+    return tried || mbar_wait(bar, parity);
+}
 // 32 lanes x N consecutive fp32 columns, no wait.
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
@@ -163,18 +178,22 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
     constexpr int SG = G32 ? 2 : 1;
     constexpr int SB = w4_scale_bytes(FMT), LB = SB / 8;
     constexpr int STEP = KB * W4_CHUNK_BYTES + SG * SB;
-    constexpr int NA = TW_NA, NW = tw_w_stages(KB);
+    constexpr int NA = TW_NA, NW = tw_w_stages(NTOK, KB, SG, FMT);
     constexpr int WST = tw_w_stage(KB, SG, FMT);
     constexpr int XSUB = NTOK * 128;       // bytes of 64 k of x
     constexpr int NC = NTOK / 2;           // columns per summing warp
-    constexpr int NB = 4;                  // accumulators in TMEM
+    constexpr int NR = tw_round(NTOK);     // tokens per round of a tile's end
+    // TMEM holds two pairs of groups' accumulators; a pair is waited for, read and
+    // given back at once (a wait that finds its barrier done still takes about 107
+    // cycles, a good part of a group's products)
+    constexpr int NB = 2;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sa = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t* sx = sa + NA * TW_SUB;
-    float* sp = (float*)(sx + NA * XSUB);  // [token][row] sums of a finished tile
-    uint8_t* sw = (uint8_t*)sp + NTOK * TW_ROWS * 4;
+    float* sp = (float*)(sx + NA * XSUB);  // [token][row] sums of a round
+    uint8_t* sw = (uint8_t*)sp + NR * TW_ROWS * 4;
     uint64_t* bars = (uint64_t*)(sw + NW * WST);
-    uint32_t* s_tmem = (uint32_t*)(bars + 40);
+    uint32_t* s_tmem = (uint32_t*)(bars + 48);
     // a summing warp gave up before a tile's first, second barrier: each is set on
     // one side of a barrier and read on the other, so all eight leave together
     volatile int* s_fail = (volatile int*)(s_tmem + 1);
@@ -188,12 +207,12 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
                    empty = full + 8 * NA, tfull = empty + 8 * NA, tempty = tfull + 8 * NB,
                    mdone = tempty + 8 * NB, pready = mdone + 8, pfree = pready + 8;
     // full: a chunk's A tile (one arrival per code warp) and x (one, and its bytes)
-    static_assert(2 * NW + 2 * NA + 2 * NB + 3 <= 40, "barriers");
+    static_assert(2 * NW + 2 * NA + 2 * NB + 3 <= 48, "barriers");
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NW; ++i) {
             mbar_init(wfull + 8 * i, 1);
-            mbar_init(wempty + 8 * i, TW_DEQ / 2 * KB + TW_SUM);
+            mbar_init(wempty + 8 * i, TW_DEQ / 2 * KB);
         }
         for (int i = 0; i < NA; ++i) {
             mbar_init(full + 8 * i, TW_DEQ / 2 + 1);
@@ -209,7 +228,7 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
         mbar_fence_init();
         s_fail[0] = s_fail[1] = 0;
     }
-    constexpr uint32_t NCOLS = NB * NTOK;
+    constexpr uint32_t NCOLS = NB * 2 * NTOK;
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(s_tmem)),
@@ -225,9 +244,24 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 0 && lane == 0) {
-            // ---------------- packed weights
+            // ---------------- packed weights; L2 is asked for them TW_PREFETCH steps
+            // ahead, so that the ring need only cover its latency, not DRAM's
             int i = 0;
             bool ok = true;
+            int64_t ptile = cl;
+            int ps = 0;
+            auto prefetch = [&]() {
+                if (ptile >= a.tiles) return;
+                const uint8_t* p = a.packed + w4_block(ptile / a.tt * 4, a.steps, k0 + ps, STEP);
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(WST) : "memory");
+                if (++ps == nst) {
+                    ps = 0;
+                    ptile += a.C;
+                }
+            };
+            for (int q = 0; q < NW + TW_PREFETCH; ++q)
+                if (q >= NW) prefetch();
+                else if (++ps == nst) ps = 0, ptile += a.C;
             for (int64_t tile = cl; tile < a.tiles && ok; tile += a.C) {
                 const uint8_t* src = a.packed + w4_block(tile / a.tt * 4, a.steps, k0, STEP);
                 for (int s = 0; s < nst; ++s, ++i, src += WST) {
@@ -238,6 +272,7 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
                         break;
                     }
                     bulk_g2s(smem_u32(sw + w * WST), src, WST, wfull + 8 * w);
+                    prefetch();
                 }
             }
             // the last copies have landed before the CTA may leave
@@ -266,45 +301,45 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
         } else if (warp == 1) {
             // ---------------- MMA issuer: the whole warp waits, one lane issues
             const uint32_t elected = elect_lane();
-            int st = 0, buf = 0;
+            int st = 0, pb = 0;
             uint32_t par = 0, tpar = 1;  // phases of the operand ring and (waited for) of TMEM
-            bool ok = true;
+            bool ok = true, tried = false;
             for (int64_t tile = cl; tile < a.tiles && ok; tile += a.C) {
                 const int64_t left = a.tokens - (tile % a.tt) * NTOK;
                 const uint32_t idesc =
                     instr_desc(TW_ROWS, (int)min((int64_t)NTOK, (left + 15) / 16 * 16));
                 for (int s = 0; s < nst && ok; ++s) {
+                    // a pair of groups: two steps, or a step of two groups; its
+                    // accumulators have been read (their first use: the phase before
+                    // the first counts as done)
+                    const bool opens = SG == 2 || s % 2 == 0, closes = SG == 2 || s % 2 == 1 || s + 1 == nst;
+                    if (opens) ok = mbar_wait(tempty + 8 * pb, tpar);
+                    const uint32_t d0 = tmem + (uint32_t)((2 * pb + (opens ? 0 : 1)) * NTOK);
 #pragma unroll
                     for (int c = 0; c < KB; ++c) {
-                        ok = ok && mbar_wait(full + 8 * st, par);
+                        ok = ok && mbar_settle(tried, full + 8 * st, par);
+                        if (!ok) break;
+                        tc_fence_after();
                         const uint64_t ao = smem_desc(smem_u32(sa + st * TW_SUB));
                         const uint64_t xo = smem_desc(smem_u32(sx + st * XSUB));
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) {
-                            // a group's part of the step starts: every two products, or
-                            // once a step; its accumulator has been read (its first use:
-                            // the phase before the first counts as done)
-                            const bool first = G32 ? kk % 2 == 0 : kk == 0 && c == 0;
-                            const bool last = G32 ? kk % 2 == 1 : kk == 3 && c == KB - 1;
-                            if (first) ok = ok && mbar_wait(tempty + 8 * buf, tpar);
-                            if (!ok) break;
-                            if (first || kk == 0) tc_fence_after();
-                            mma_bf16_elect(elected, tmem + (uint32_t)(buf * NTOK), ao + 2 * kk, xo + 2 * kk,
-                                           idesc, first ? 0u : 1u);
-                            if (last) {
-                                mma_commit_elect(elected, tfull + 8 * buf);
-                                if (++buf == NB) {
-                                    buf = 0;
-                                    tpar ^= 1u;
-                                }
-                            }
-                        }
-                        if (!ok) break;
-                        mma_commit_elect(elected, empty + 8 * st);
+                        const uint32_t done = empty + 8 * st;
                         if (++st == NA) {
                             st = 0;
                             par ^= 1u;
                         }
+                        tried = mbar_test(full + 8 * st, par);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+                            const bool first = SG == 2 ? kk % 2 == 0 : kk == 0 && c == 0;
+                            mma_bf16_elect(elected, d0 + (SG == 2 ? kk / 2 * NTOK : 0), ao + 2 * kk, xo + 2 * kk,
+                                           idesc, first ? 0u : 1u);
+                        }
+                        mma_commit_elect(elected, done);
+                    }
+                    if (ok && closes) {
+                        mma_commit_elect(elected, tfull + 8 * pb);
+                        pb ^= 1;
+                        if (pb == 0) tpar ^= 1u;
                     }
                 }
             }
@@ -312,7 +347,7 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
             mma_commit_elect(elected, mdone);  // fires when every MMA issued has completed
         }
     } else if (warp < 4 + TW_DEQ) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         // ---------------- codes to operands: a warp takes a half block (16 rows x 64 k)
         // of every other chunk
         const int d = (warp - 4) & 7, grp = (warp - 4) >> 3;
@@ -331,23 +366,36 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
         left = (left - grp + 1) / 2;
         int w = KB == 2 ? 0 : grp % NW;
         uint32_t wpar = 0;
+        // Tested while the chunk before was worked on.  A test by parity must not come
+        // two phases early: A's stage was waited for two chunks ago; W's step i - NW
+        // had landed when chunk i - 6 was multiplied, which this warp has waited for.
+        static_assert(KB == 2 || NW >= 6, "the phase before is complete");
+        bool w_ready = false, a_ready = false;
         for (int k = 0; k < left; ++k) {
             const int st = grp + 2 * (k & 1);  // chunk 2 k + grp, stage by its number mod 4
             static_assert(NA == 4, "two stages for either half");
-            if (!mbar_wait(wfull + 8 * w, wpar) ||
-                (k >= 2 && !mbar_wait(empty + 8 * st, ((k >> 1) - 1) & 1))) {
+            if (!mbar_settle(w_ready, wfull + 8 * w, wpar) ||
+                (k >= 2 && !mbar_settle(a_ready, empty + 8 * st, ((k >> 1) - 1) & 1))) {
                 if (lane == 0) atomicOr(&g_dev_err, ERR_EPILOGUE);
                 break;
             }
             const uint4 v = *(const uint4*)(src + w * WST + (KB == 2 ? grp * W4_CHUNK_BYTES : 0));
+            const int w_at = w;
+            w += KB == 2 ? 1 : 2;
+            if (w >= NW) {
+                w -= NW;
+                wpar ^= 1u;
+            }
+            w_ready = mbar_test(wfull + 8 * w, wpar);
+            a_ready = mbar_test(empty + 8 * (grp + 2 * ((k + 1) & 1)), (((k + 1) >> 1) - 1) & 1);
             uint32_t z[2][2];  // [half of the 64 k][row r, r + 8]
             z[0][0] = z[0][1] = z[1][0] = z[1][1] = 0x41C041C0u;  // 16 + 8
             if constexpr (FMT != 0) {
-                const uint32_t q = *(const uint32_t*)(zsrc + w * WST);
+                const uint32_t q = *(const uint32_t*)(zsrc + w_at * WST);
                 z[0][0] = z[1][0] = __byte_perm(q, 0, 0x1010);
                 z[0][1] = z[1][1] = __byte_perm(q, 0, 0x3232);
                 if constexpr (G32) {
-                    const uint32_t q1 = *(const uint32_t*)(zsrc + w * WST + SB);
+                    const uint32_t q1 = *(const uint32_t*)(zsrc + w_at * WST + SB);
                     z[1][0] = __byte_perm(q1, 0, 0x1010);
                     z[1][1] = __byte_perm(q1, 0, 0x3232);
                 }
@@ -369,182 +417,207 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(full + 8 * st);
-                mbar_arrive(wempty + 8 * w);
-            }
-            w += KB == 2 ? 1 : 2;
-            if (w >= NW) {
-                w -= NW;
-                wpar ^= 1u;
+                mbar_arrive(wempty + 8 * w_at);
             }
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
         // ---------------- scaling and sums
         const int q = warp & 3;                     // TMEM lanes 32 q .. 32 q + 31 = unit q
         const int half = (warp - 4 - TW_DEQ) >> 2;  // columns half * NC ..
         const int e = threadIdx.x - 32 * (4 + TW_DEQ);
         const uint32_t tb = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(half * NC);
-        const int srow = (lane & 7) * LB, sj = lane >> 3;  // this row's scale
-        int w = 0, buf = 0, ntile = 0;
-        uint32_t wpar = 0, tpar = 0;
-        bool ok = true;
-        for (int64_t tile = cl; tile < a.tiles; tile += a.C, ++ntile) {
-            const int64_t rt = tile / a.tt;
-            const int64_t tok0 = (tile - rt * a.tt) * NTOK;
+        int round = 0, pb = 0;
+        uint32_t tpar = 0;
+        bool ok = true, tried = false;
+        for (int64_t tile = cl; tile < a.tiles; tile += a.C) {
+            const int rt = (int)(tile / a.tt);
+            const int tok0 = (int)(tile - (int64_t)rt * a.tt) * NTOK;
             const int ntok = (int)min((int64_t)NTOK, a.tokens - tok0);
+            // this row's scales, TW_AHEAD steps ahead of their use, straight from the
+            // packed steps (in L2 by then)
+            const uint8_t* sp0 = a.packed + w4_block((int64_t)rt * 4 + q, a.steps, k0, STEP) + KB * W4_CHUNK_BYTES +
+                                 (lane & 7) * LB + (lane >> 3) * ((FMT & DFLASH2_W4_SCALE_F32) ? 4 : 2);
+            auto read_scales = [&](int s, float (&f)[SG]) {
+                const uint8_t* p = sp0 + (int64_t)min(s, nst - 1) * WST;
+#pragma unroll
+                for (int h = 0; h < SG; ++h) {
+                    if constexpr ((FMT & DFLASH2_W4_SCALE_F32) != 0)
+                        f[h] = __ldg((const float*)(p + h * SB));
+                    else
+                        f[h] = __uint_as_float((uint32_t)__ldg((const unsigned short*)(p + h * SB)) << 16);
+                }
+            };
+            constexpr int PS = SG == 1 ? 2 : 1;  // steps of a pair of groups
+            float sc[TW_AHEAD][SG];              // of the steps from s on
+#pragma unroll
+            for (int s = 0; s < TW_AHEAD; ++s) read_scales(s, sc[s]);
             uint64_t acc[NC / 2];  // pairs of tokens
 #pragma unroll
             for (int n = 0; n < NC / 2; ++n) acc[n] = 0;
-            for (int s = 0; s < nst && ok; ++s) {
-                float sc[SG];
-                ok = mbar_wait(wfull + 8 * w, wpar);
-                if (ok) {
-                    const uint8_t* p = sw + w * WST + q * STEP + KB * W4_CHUNK_BYTES + srow;
+            for (int s = 0; s < nst; s += PS) {
+                ok = mbar_settle(tried, tfull + 8 * pb, tpar);
+                if (!ok) break;
+                tc_fence_after();
+                const int done = pb;
+                pb ^= 1;
+                if (pb == 0) tpar ^= 1u;
+                tried = mbar_test(tfull + 8 * pb, tpar);
+                const uint32_t ta = tb + (uint32_t)(done * 2 * NTOK);
+                // (an odd last step of a tile goes alone)
 #pragma unroll
-                    for (int h = 0; h < SG; ++h) {
-                        if constexpr ((FMT & DFLASH2_W4_SCALE_F32) != 0)
-                            sc[h] = ((const float*)(p + h * SB))[sj];
-                        else
-                            sc[h] = __uint_as_float((uint32_t)((const unsigned short*)(p + h * SB))[sj] << 16);
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(wempty + 8 * w);
-                    if (++w == NW) {
-                        w = 0;
-                        wpar ^= 1u;
-                    }
-                }
-#pragma unroll
-                for (int h = 0; h < SG; ++h) {
-                    ok = ok && mbar_wait(tfull + 8 * buf, tpar);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t ta = tb + (uint32_t)(buf * NTOK);
+                for (int g = 0; g < 2; ++g) {
+                    const float f = SG == 2 ? sc[0][g % SG] : sc[g % PS][0];
                     constexpr int G = NC >= 32 ? 2 : 1;  // 16-column loads in flight
+                    if (SG == 2 || g == 0 || s + 1 < nst)
 #pragma unroll
-                    for (int n = 0; n < NC; n += 16 * G) {
-                        if (half * NC + n < ntok) {  // the same for the whole warp
-                            uint32_t v[G][16];
+                        for (int n = 0; n < NC; n += 16 * G) {
+                            if (half * NC + n < ntok) {  // the same for the whole warp
+                                uint32_t v[G][16];
 #pragma unroll
-                            for (int g = 0; g < G; ++g) tmem_ld(ta + n + 16 * g, v[g]);
-                            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                                for (int z = 0; z < G; ++z) tmem_ld(ta + g * NTOK + n + 16 * z, v[z]);
+                                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-                            for (int g = 0; g < G; ++g)
+                                for (int z = 0; z < G; ++z)
 #pragma unroll
-                                for (int z = 0; z < 16; z += 2) {
-                                    uint64_t& p = acc[(n + 16 * g + z) / 2];
-                                    p = f2_fma(f2_pack(sc[h], sc[h]),
-                                               f2_pack(__uint_as_float(v[g][z]), __uint_as_float(v[g][z + 1])), p);
-                                }
+                                    for (int x = 0; x < 16; x += 2) {
+                                        uint64_t& p = acc[(n + 16 * z + x) / 2];
+                                        p = f2_fma(f2_pack(f, f),
+                                                   f2_pack(__uint_as_float(v[z][x]), __uint_as_float(v[z][x + 1])),
+                                                   p);
+                                    }
+                            }
                         }
-                    }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(tempty + 8 * buf);
-                    if (++buf == NB) {
-                        buf = 0;
-                        tpar ^= 1u;
-                    }
                 }
-            }
-            // the tile's sums of this CTA's K, then of the cluster's
-            if (ok && a.S > 1 && ntile > 0) ok = cluster_wait(pfree, (ntile - 1) & 1);
-            if (!ok) {
-                atomicOr(&g_dev_err, (unsigned)ERR_EPILOGUE);
-                s_fail[0] = 1;
-            } else {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(tempty + 8 * done);
 #pragma unroll
-                for (int n = 0; n < NC; n += 2) {
-                    sp[(half * NC + n) * TW_ROWS + 32 * q + lane] = f2_lo(acc[n / 2]);
-                    sp[(half * NC + n + 1) * TW_ROWS + 32 * q + lane] = f2_hi(acc[n / 2]);
-                }
+                for (int z = 0; z + PS < TW_AHEAD; ++z)
+#pragma unroll
+                    for (int h = 0; h < SG; ++h) sc[z][h] = sc[z + PS][h];
+#pragma unroll
+                for (int z = 0; z < PS; ++z) read_scales(s + TW_AHEAD + z, sc[TW_AHEAD - PS + z]);
             }
-            asm volatile("bar.sync 1, 256;" ::: "memory");
-            if (s_fail[0]) break;
-            if (a.S > 1) {
-                if (e < a.S) cluster_arrive(pready, e);
-                ok = cluster_wait(pready, ntile & 1);
-                if (!ok) {
-                    atomicOr(&g_dev_err, (unsigned)ERR_EPILOGUE);
-                    s_fail[1] = 1;
-                }
-            }
-            // this CTA writes its share of the tokens
-            const int t0 = NTOK * rank / a.S, t1 = min(NTOK * (rank + 1) / a.S, ntok);
-            // four rows of a token at a time, four such items in flight
+            // the tile's sums of this CTA's K, then of the cluster's, NR tokens at a
+            // time; this CTA writes its share of each round
+            const int share = NR / a.S;
             const uint32_t spu = smem_u32(sp);
-            auto sum4 = [&](int row, int t, float (&v)[4]) {
-                const uint32_t o = spu + 4 * (t * TW_ROWS + row);
-                v[0] = v[1] = v[2] = v[3] = 0.0f;
+            // four rows of M items' tokens: every item's part from one CTA before the
+            // next CTA's, so that the reads are in flight together
+            auto sum4 = [&](auto& v, int row, int t, int dt, int last) {
+                constexpr int M = sizeof(v) / sizeof(v[0]);
+#pragma unroll
+                for (int z = 0; z < M; ++z) v[z] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 for (int k = 0; k < a.S; ++k) {
-                    const float4 f = ld_cluster4(o, k);
-                    v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
+                    float4 f[M];
+#pragma unroll
+                    for (int z = 0; z < M; ++z)
+                        f[z] = ld_cluster4(spu + 4 * (min(t + dt * z, last) * TW_ROWS + row), k);
+#pragma unroll
+                    for (int z = 0; z < M; ++z)
+                        v[z].x += f[z].x, v[z].y += f[z].y, v[z].z += f[z].z, v[z].w += f[z].w;
                 }
             };
-            if (ok && !a.x_prev) {
-                const int row = (e & 31) * 4;
-                const int64_t n = rt * TW_ROWS + row;
-                for (int t = t0 + (e >> 5); t < t1; t += 32) {
-                    float v[4][4];
+            const int rounds = (ntok + NR - 1) / NR;  // the same in every CTA of the cluster
+            for (int rd = 0; rd < rounds; ++rd, ++round) {
+                const int t0 = share * rank, t1 = min(t0 + share, ntok - rd * NR);
+                const int tokr = tok0 + rd * NR;  // the round's first token
+                if (ok && a.S > 1 && round > 0) ok = cluster_wait(pfree, (round - 1) & 1);
+                if (!ok) {
+                    atomicOr(&g_dev_err, (unsigned)ERR_EPILOGUE);
+                    s_fail[0] = 1;
+                } else if (NR == NTOK || half == rd) {
+                    float* d = sp + (NR == NTOK ? half * NC : 0) * TW_ROWS + 32 * q + lane;
 #pragma unroll
-                    for (int z = 0; z < 4; ++z) sum4(row, min(t + 8 * z, t1 - 1), v[z]);
+                    for (int n = 0; n < NC; n += 2) {
+                        d[n * TW_ROWS] = f2_lo(acc[n / 2]);
+                        d[(n + 1) * TW_ROWS] = f2_hi(acc[n / 2]);
+                    }
+                }
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                if (s_fail[0]) break;
+                if (a.S > 1 && e < a.S) cluster_arrive(pready, e);
+                auto joined = [&]() {
+                    if (a.S > 1) ok = cluster_wait(pready, round & 1);
+                    if (!ok) {
+                        atomicOr(&g_dev_err, (unsigned)ERR_EPILOGUE);
+                        s_fail[1] = 1;
+                    }
+                };
+                if (!a.x_prev) {
+                    const int row = (e & 31) * 4;
+                    const int64_t n = (int64_t)rt * TW_ROWS + row;
+                    const int64_t o0 = tokr * a.ld + n;
+                    joined();
+                    for (int t = t0 + (e >> 5); t < t1 && ok; t += 32) {
+                        float4 v[4];
+                        sum4(v, row, t, 8, t1 - 1);
 #pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        if (t + 8 * z >= t1) break;
-                        const int64_t o = (tok0 + t + 8 * z) * a.ld + n;
-                        if (a.y_vec && n + 4 <= a.n_rows) {
-                            if (a.y_bf16)
-                                *(uint2*)((__nv_bfloat16*)a.y + o) = pack4(v[z]);
-                            else
-                                *(float4*)((float*)a.y + o) = make_float4(v[z][0], v[z][1], v[z][2], v[z][3]);
-                        } else {
+                        for (int z = 0; z < 4; ++z) {
+                            if (t + 8 * z >= t1) break;
+                            const int64_t o = o0 + (t + 8 * z) * a.ld;
+                            const float w4[4] = {v[z].x, v[z].y, v[z].z, v[z].w};
+                            if (a.y_vec && n + 4 <= a.n_rows) {
+                                if (a.y_bf16)
+                                    *(uint2*)((__nv_bfloat16*)a.y + o) = pack4(w4);
+                                else
+                                    *(float4*)((float*)a.y + o) = v[z];
+                            } else {
 #pragma unroll
-                            for (int p = 0; p < 4; ++p)
-                                if (n + p < a.n_rows) {
-                                    if (a.y_bf16)
-                                        ((__nv_bfloat16*)a.y)[o + p] = __float2bfloat16_rn(v[z][p]);
-                                    else
-                                        ((float*)a.y)[o + p] = v[z][p];
-                                }
+                                for (int p = 0; p < 4; ++p)
+                                    if (n + p < a.n_rows) {
+                                        if (a.y_bf16)
+                                            ((__nv_bfloat16*)a.y)[o + p] = __float2bfloat16_rn(w4[p]);
+                                        else
+                                            ((float*)a.y)[o + p] = w4[p];
+                                    }
+                            }
                         }
                     }
-                }
-            } else if (ok) {
-                // a and b of a channel: rows 8 apart (w4_pack, taps); H is a multiple
-                // of 64, so a tile's 64 channels are all there
-                const int c4 = (e & 15) * 4, row = (c4 >> 3) * 16 + (c4 & 7);
-                const int64_t ch = rt * 64 + c4;
-                for (int t = t0 + (e >> 4); t < t1; t += 32) {
-                    float av[2][4], bv[2][4];
+                } else {
+                    // a and b of a channel: rows 8 apart (w4_pack, taps); H is a multiple
+                    // of 64, so a tile's 64 channels are all there
+                    const int c4 = (e & 15) * 4, row = (c4 >> 3) * 16 + (c4 & 7);
+                    const int ch = rt * 64 + c4;
                     uint2 xc[2], xp[2];
+                    auto load_x = [&](int t) {
 #pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        const int64_t tok = tok0 + min(t + 16 * z, t1 - 1);
-                        xc[z] = *(const uint2*)(a.x + tok * a.ld + ch);
-                        xp[z] = *(const uint2*)(tok % a.T == 0 ? a.x_prev + tok / a.T * a.ld + ch
-                                                               : a.x + (tok - 1) * a.ld + ch);
-                    }
+                        for (int z = 0; z < 2; ++z) {
+                            const int tok = tokr + min(t + 16 * z, t1 - 1), sq = tok / a.T;
+                            const __nv_bfloat16* x = a.x + tok * a.ld + ch;
+                            xc[z] = __ldg((const uint2*)x);
+                            xp[z] = __ldg((const uint2*)(tok == sq * a.T ? a.x_prev + sq * a.ld + ch : x - a.ld));
+                        }
+                    };
+                    int t = t0 + (e >> 4);
+                    if (t < t1) load_x(t);  // on its way while the cluster's sums come in
+                    joined();
+                    for (; t < t1 && ok; t += 32) {
+                        float4 av[2], bv[2];
+                        sum4(av, row, t, 16, t1 - 1);
+                        sum4(bv, row + 8, t, 16, t1 - 1);
 #pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        sum4(row, min(t + 16 * z, t1 - 1), av[z]);
-                        sum4(row + 8, min(t + 16 * z, t1 - 1), bv[z]);
-                    }
+                        for (int z = 0; z < 2; ++z) {
+                            if (t + 16 * z >= t1) break;
+                            const float a4[4] = {av[z].x, av[z].y, av[z].z, av[z].w};
+                            const float b4[4] = {bv[z].x, bv[z].y, bv[z].z, bv[z].w};
+                            float c[4], p[4];
+                            unpack4(xc[z], c);
+                            unpack4(xp[z], p);
 #pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        if (t + 16 * z >= t1) break;
-                        float c[4], p[4];
-                        unpack4(xc[z], c);
-                        unpack4(xp[z], p);
-#pragma unroll
-                        for (int q2 = 0; q2 < 4; ++q2)
-                            c[q2] = fmaf(bv[z][q2], p[q2], fmaf(av[z][q2], c[q2], c[q2]));
-                        *(uint2*)((__nv_bfloat16*)a.y + (tok0 + t + 16 * z) * a.ld + ch) = pack4(c);
+                            for (int q2 = 0; q2 < 4; ++q2)
+                                c[q2] = fmaf(b4[q2], p[q2], fmaf(a4[q2], c[q2], c[q2]));
+                            *(uint2*)((__nv_bfloat16*)a.y + (int64_t)(tokr + t + 16 * z) * a.ld + ch) = pack4(c);
+                        }
+                        if (t + 32 < t1) load_x(t + 32);
                     }
                 }
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                if (s_fail[1]) break;
+                if (a.S > 1 && e < a.S) cluster_arrive(pfree, e);
             }
-            asm volatile("bar.sync 1, 256;" ::: "memory");
-            if (s_fail[1]) break;
-            if (a.S > 1 && e < a.S) cluster_arrive(pfree, e);
+            if (s_fail[0] || s_fail[1]) break;
         }
     }
     __syncthreads();
