@@ -87,6 +87,9 @@ __device__ __forceinline__ void tw_load_x(uint32_t dst, const CUtensorMap* map, 
         "l"(map), "r"(k), "r"(tok), "r"(bar)
         : "memory");
 }
+__device__ __forceinline__ void prefetch_l2(const void* p, int bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void cluster_arrive(uint32_t bar, int rank) {
     asm volatile(
         "{\n\t.reg .b32 r;\n\t"
@@ -237,7 +240,9 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
         tc_fence_before();
     }
     __syncthreads();
-    if (a.S > 1) cg::this_cluster().sync();  // the barriers of every CTA are set up
+    // the barriers of every CTA are set up: waited for before the first use of
+    // another CTA's
+    if (a.S > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
 
@@ -245,34 +250,31 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 0 && lane == 0) {
             // ---------------- packed weights; L2 is asked for them TW_PREFETCH steps
-            // ahead, so that the ring need only cover its latency, not DRAM's
+            // before their copy, four at a time, so that the ring need only cover its
+            // latency, not DRAM's
             int i = 0;
             bool ok = true;
-            int64_t ptile = cl;
-            int ps = 0;
-            auto prefetch = [&]() {
-                if (ptile >= a.tiles) return;
-                const uint8_t* p = a.packed + w4_block(ptile / a.tt * 4, a.steps, k0 + ps, STEP);
-                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(WST) : "memory");
-                if (++ps == nst) {
-                    ps = 0;
-                    ptile += a.C;
-                }
-            };
-            for (int q = 0; q < NW + TW_PREFETCH; ++q)
-                if (q >= NW) prefetch();
-                else if (++ps == nst) ps = 0, ptile += a.C;
             for (int64_t tile = cl; tile < a.tiles && ok; tile += a.C) {
                 const uint8_t* src = a.packed + w4_block(tile / a.tt * 4, a.steps, k0, STEP);
-                for (int s = 0; s < nst; ++s, ++i, src += WST) {
+                const int64_t next = tile + a.C;
+                const uint8_t* src1 =
+                    a.packed + w4_block((next < a.tiles ? next : tile) / a.tt * 4, a.steps, k0, STEP);
+                for (int s = 0; s < nst; ++s, ++i) {
                     const int w = i % NW;
                     if (i >= NW && !mbar_wait(wempty + 8 * w, (i / NW - 1) & 1)) {
                         atomicOr(&g_dev_err, ERR_PRODUCER);
                         ok = false;
                         break;
                     }
-                    bulk_g2s(smem_u32(sw + w * WST), src, WST, wfull + 8 * w);
-                    prefetch();
+                    bulk_g2s(smem_u32(sw + w * WST), src + (int64_t)s * WST, WST, wfull + 8 * w);
+                    if (s % 4 == 3 && i >= NW - 1) {
+                        // steps s + TW_PREFETCH .. of this tile or, past its end, of the next
+                        const int p = s + TW_PREFETCH, over = p - nst;
+                        if (over < 0)
+                            prefetch_l2(src + (int64_t)p * WST, min(4, -over) * WST);
+                        else if (next < a.tiles && over < nst)
+                            prefetch_l2(src1 + (int64_t)over * WST, min(4, nst - over) * WST);
+                    }
                 }
             }
             // the last copies have landed before the CTA may leave
@@ -427,6 +429,7 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
         const int half = (warp - 4 - TW_DEQ) >> 2;  // columns half * NC ..
         const int e = threadIdx.x - 32 * (4 + TW_DEQ);
         const uint32_t tb = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(half * NC);
+        if (a.S > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
         int round = 0, pb = 0;
         uint32_t tpar = 0;
         bool ok = true, tried = false;
@@ -619,6 +622,10 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
             }
             if (s_fail[0] || s_fail[1]) break;
         }
+    }
+    if (a.S > 1 && warp < 4 + TW_DEQ) {
+        __syncwarp();
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
     __syncthreads();
     if (warp == 1) {
