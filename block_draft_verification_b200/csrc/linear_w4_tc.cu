@@ -6,8 +6,8 @@
 //                ring
 //   warp 2       TMA of the tokens' x (64 k boxes, 128-byte swizzle) into the X ring
 //   warps 4-19   codes to exact bf16 integers q - zero, stored as the K-major,
-//                128-byte swizzled A tile of a 64 k chunk; the two halves of these
-//                warps take chunks in turn
+//                128-byte swizzled A tile of a 64 k chunk; a warp takes a unit, and
+//                each four warps every fourth chunk
 //   warp 1       tcgen05.mma (M = 128, N = tokens, K = 16) of a group's k into one
 //                of four TMEM accumulators
 //   warps 20-27  tcgen05.ld of the group's sums, times the row's scale, added to
@@ -86,6 +86,21 @@ __device__ __forceinline__ void tw_load_x(uint32_t dst, const CUtensorMap* map, 
         " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
         "l"(map), "r"(k), "r"(tok), "r"(bar)
         : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 __device__ __forceinline__ void prefetch_l2(const void* p, int bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
@@ -215,10 +230,10 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < NW; ++i) {
             mbar_init(wfull + 8 * i, 1);
-            mbar_init(wempty + 8 * i, TW_DEQ / 2 * KB);
+            mbar_init(wempty + 8 * i, 4 * KB);
         }
         for (int i = 0; i < NA; ++i) {
-            mbar_init(full + 8 * i, TW_DEQ / 2 + 1);
+            mbar_init(full + 8 * i, 4 + 1);
             mbar_init(empty + 8 * i, 1);
         }
         for (int i = 0; i < NB; ++i) {
@@ -350,76 +365,69 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
         }
     } else if (warp < 4 + TW_DEQ) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-        // ---------------- codes to operands: a warp takes a half block (16 rows x 64 k)
-        // of every other chunk
-        const int d = (warp - 4) & 7, grp = (warp - 4) >> 3;
-        const int u = d >> 1, b = d & 1;
+        // ---------------- codes to operands: a warp takes a unit's 32 rows of every
+        // fourth chunk, always into the same stage of A
+        static_assert(NA == 4 && TW_DEQ == 16, "a stage for each four warps");
+        const int u = warp & 3, grp = (warp - 4) >> 2;
         const int r = lane >> 2, c = lane & 3;
         const bool odd = (r & 1) != 0;  // odd rows store their second half first: the
                                         // eight lanes of a store then hit all banks
-        const int o0 = ((4 * (odd ? 1 : 0) + c) ^ r) * 16, o1 = ((4 * (odd ? 0 : 1) + c) ^ r) * 16;
-        const uint8_t* src = sw + u * STEP + b * 512 + lane * 16;
-        // the zero points of rows r and r + 8 of this half
-        const uint8_t* zsrc = sw + u * STEP + KB * W4_CHUNK_BYTES + r * LB +
-                              ((FMT & DFLASH2_W4_SCALE_F32) ? 16 : 8) + 4 * b;
-        uint8_t* dst0 = sa + (u * 32 + b * 16 + r) * 128;
-        int left = 0;  // chunks of this CTA's tiles that this half of the warps takes
+        const uint32_t src = smem_u32(sw) + u * STEP + lane * 16 + (KB == 2 ? (grp & 1) * W4_CHUNK_BYTES : 0);
+        // the zero points of the lane's rows r, r + 8, r + 16, r + 24
+        const uint32_t zsrc = smem_u32(sw) + u * STEP + KB * W4_CHUNK_BYTES + r * LB +
+                              ((FMT & DFLASH2_W4_SCALE_F32) ? 16 : 8);
+        const uint32_t dst = smem_u32(sa) + grp * TW_SUB + (u * 32 + r) * 128;
+        const uint32_t d0 = dst + ((4 * (odd ? 1 : 0) + c) ^ r) * 16, d1 = dst + ((4 * (odd ? 0 : 1) + c) ^ r) * 16;
+        int left = 0;  // chunks of this CTA's tiles that these four warps take
         for (int64_t tile = cl; tile < a.tiles; tile += a.C) left += nst * KB;
-        left = (left - grp + 1) / 2;
-        int w = KB == 2 ? 0 : grp % NW;
-        uint32_t wpar = 0;
-        // Tested while the chunk before was worked on.  A test by parity must not come
-        // two phases early: A's stage was waited for two chunks ago; W's step i - NW
-        // had landed when chunk i - 6 was multiplied, which this warp has waited for.
-        static_assert(KB == 2 || NW >= 6, "the phase before is complete");
-        bool w_ready = false, a_ready = false;
+        left = (left - grp + 3) / 4;
+        int w = (KB == 2 ? grp >> 1 : grp) % NW;
+        uint32_t wpar = 0, apar = 1;  // A's stage: the phase before the first counts as done
+        // W is tested while the chunk before is worked on.  A test by parity must not
+        // come two phases early: chunk i - 4, waited for here, had its W, and a stage's
+        // use before is no later than that one's
+        static_assert(KB == 2 ? NW >= 4 : NW >= 8, "the phase before is complete");
+        bool ready = false;
         for (int k = 0; k < left; ++k) {
-            const int st = grp + 2 * (k & 1);  // chunk 2 k + grp, stage by its number mod 4
-            static_assert(NA == 4, "two stages for either half");
-            if (!mbar_settle(w_ready, wfull + 8 * w, wpar) ||
-                (k >= 2 && !mbar_settle(a_ready, empty + 8 * st, ((k >> 1) - 1) & 1))) {
+            if (!mbar_settle(ready, wfull + 8 * w, wpar) || !mbar_wait(empty + 8 * grp, apar)) {
                 if (lane == 0) atomicOr(&g_dev_err, ERR_EPILOGUE);
                 break;
             }
-            const uint4 v = *(const uint4*)(src + w * WST + (KB == 2 ? grp * W4_CHUNK_BYTES : 0));
-            const int w_at = w;
-            w += KB == 2 ? 1 : 2;
+            apar ^= 1u;
+            const uint32_t wo = (uint32_t)(w * WST), wdone = wempty + 8 * w;
+            const uint4 v[2] = {lds128(src + wo), lds128(src + wo + 512)};
+            uint2 zq[SG];
+            if constexpr (FMT != 0)
+#pragma unroll
+                for (int h = 0; h < SG; ++h) zq[h] = lds64(zsrc + wo + h * SB);
+            w += KB == 2 ? 2 : 4;
             if (w >= NW) {
                 w -= NW;
                 wpar ^= 1u;
             }
-            w_ready = mbar_test(wfull + 8 * w, wpar);
-            a_ready = mbar_test(empty + 8 * (grp + 2 * ((k + 1) & 1)), (((k + 1) >> 1) - 1) & 1);
-            uint32_t z[2][2];  // [half of the 64 k][row r, r + 8]
-            z[0][0] = z[0][1] = z[1][0] = z[1][1] = 0x41C041C0u;  // 16 + 8
-            if constexpr (FMT != 0) {
-                const uint32_t q = *(const uint32_t*)(zsrc + w_at * WST);
-                z[0][0] = z[1][0] = __byte_perm(q, 0, 0x1010);
-                z[0][1] = z[1][1] = __byte_perm(q, 0, 0x3232);
-                if constexpr (G32) {
-                    const uint32_t q1 = *(const uint32_t*)(zsrc + w_at * WST + SB);
-                    z[1][0] = __byte_perm(q1, 0, 0x1010);
-                    z[1][1] = __byte_perm(q1, 0, 0x3232);
-                }
-            }
-            uint8_t* dst = dst0 + st * TW_SUB;
+            ready = mbar_test(wfull + 8 * w, wpar);
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const uint32_t wa = q == 0 ? (odd ? v.y : v.x) : (odd ? v.w : v.z);
-                const uint32_t wb = q == 0 ? (odd ? v.x : v.y) : (odd ? v.z : v.w);
-                const uint32_t za = G32 && odd ? z[1][q] : z[0][q], zb = G32 && odd ? z[0][q] : z[1][q];
-                *(uint4*)(dst + q * 1024 + o0) =
-                    make_uint4(w4_pair_exact(wa, 0, za), w4_pair_exact(wa, 1, za),
-                               w4_pair_exact(wa, 2, za), w4_pair_exact(wa, 3, za));
-                *(uint4*)(dst + q * 1024 + o1) =
-                    make_uint4(w4_pair_exact(wb, 0, zb), w4_pair_exact(wb, 1, zb),
-                               w4_pair_exact(wb, 2, zb), w4_pair_exact(wb, 3, zb));
-            }
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {  // rows r + 16 b + 8 q
+                    uint32_t z0 = 0x41C041C0u, z1 = 0x41C041C0u;  // 16 + 8; of either half
+                    if constexpr (FMT != 0) {
+                        z0 = z1 = __byte_perm(b ? zq[0].y : zq[0].x, 0, q ? 0x3232 : 0x1010);
+                        if constexpr (G32) z1 = __byte_perm(b ? zq[SG - 1].y : zq[SG - 1].x, 0, q ? 0x3232 : 0x1010);
+                    }
+                    const uint32_t h0 = q ? v[b].z : v[b].x, h1 = q ? v[b].w : v[b].y;
+                    const uint32_t wa = odd ? h1 : h0, wb = odd ? h0 : h1;
+                    const uint32_t za = G32 && odd ? z1 : z0, zb = G32 && odd ? z0 : z1;
+                    sts128(d0 + b * 2048 + q * 1024, w4_pair_exact(wa, 0, za), w4_pair_exact(wa, 1, za),
+                           w4_pair_exact(wa, 2, za), w4_pair_exact(wa, 3, za));
+                    sts128(d1 + b * 2048 + q * 1024, w4_pair_exact(wb, 0, zb), w4_pair_exact(wb, 1, zb),
+                           w4_pair_exact(wb, 2, zb), w4_pair_exact(wb, 3, zb));
+                }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(full + 8 * st);
-                mbar_arrive(wempty + 8 * w_at);
+                mbar_arrive(full + 8 * grp);
+                mbar_arrive(wdone);
             }
         }
     } else {
