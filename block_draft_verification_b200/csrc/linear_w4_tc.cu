@@ -76,7 +76,7 @@ __host__ __device__ constexpr int tw_w_stages(int n, int kb, int sg, int fmt) {
 __host__ __device__ constexpr int tw_smem(int n, int kb, int sg, int fmt) {
     return tw_fixed(n) + tw_w_stages(n, kb, sg, fmt) * tw_w_stage(kb, sg, fmt);
 }
-constexpr int TW_AHEAD = 6;      // steps by which the scales are read before their sums
+constexpr int TW_AHEAD = 3;      // pairs of groups by which the scales are read before their sums
 constexpr int TW_PREFETCH = 12;  // steps between the request to L2 and the copy
 
 __device__ __forceinline__ void tw_load_x(uint32_t dst, const CUtensorMap* map, int k, int tok,
@@ -460,55 +460,60 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
                 }
             };
             constexpr int PS = SG == 1 ? 2 : 1;  // steps of a pair of groups
-            float sc[TW_AHEAD][SG];              // of the steps from s on
+            float sc[TW_AHEAD][PS][SG];          // of the pair at hand and the next ones, in turn
 #pragma unroll
-            for (int s = 0; s < TW_AHEAD; ++s) read_scales(s, sc[s]);
+            for (int z = 0; z < TW_AHEAD; ++z)
+#pragma unroll
+                for (int y = 0; y < PS; ++y) read_scales(z * PS + y, sc[z][y]);
             uint64_t acc[NC / 2];  // pairs of tokens
 #pragma unroll
             for (int n = 0; n < NC / 2; ++n) acc[n] = 0;
-            for (int s = 0; s < nst; s += PS) {
-                ok = mbar_settle(tried, tfull + 8 * pb, tpar);
-                if (!ok) break;
-                tc_fence_after();
-                const int done = pb;
-                pb ^= 1;
-                if (pb == 0) tpar ^= 1u;
-                tried = mbar_test(tfull + 8 * pb, tpar);
-                const uint32_t ta = tb + (uint32_t)(done * 2 * NTOK);
-                // (an odd last step of a tile goes alone)
+            // (a register that a load is still to fill is not moved: the pairs take the
+            // scale registers in turn)
+            for (int s0 = 0; s0 < nst && ok; s0 += TW_AHEAD * PS) {
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    const float f = SG == 2 ? sc[0][g % SG] : sc[g % PS][0];
-                    constexpr int G = NC >= 32 ? 2 : 1;  // 16-column loads in flight
-                    if (SG == 2 || g == 0 || s + 1 < nst)
+                for (int z0 = 0; z0 < TW_AHEAD; ++z0) {
+                    const int s = s0 + z0 * PS;
+                    if (s >= nst) break;
+                    ok = mbar_settle(tried, tfull + 8 * pb, tpar);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const int done = pb;
+                    pb ^= 1;
+                    if (pb == 0) tpar ^= 1u;
+                    tried = mbar_test(tfull + 8 * pb, tpar);
+                    const uint32_t ta = tb + (uint32_t)(done * 2 * NTOK);
 #pragma unroll
-                        for (int n = 0; n < NC; n += 16 * G) {
-                            if (half * NC + n < ntok) {  // the same for the whole warp
-                                uint32_t v[G][16];
+                    for (int g = 0; g < 2; ++g) {
+                        const float f = SG == 2 ? sc[z0][0][g % SG] : sc[z0][g % PS][0];
+                        constexpr int G = NC >= 32 ? 2 : 1;  // 16-column loads in flight
+                        if (SG == 2 || g == 0 || s + 1 < nst)  // an odd last step goes alone
 #pragma unroll
-                                for (int z = 0; z < G; ++z) tmem_ld(ta + g * NTOK + n + 16 * z, v[z]);
-                                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                            for (int n = 0; n < NC; n += 16 * G) {
+                                if (half * NC + n < ntok) {  // the same for the whole warp
+                                    uint32_t v[G][16];
 #pragma unroll
-                                for (int z = 0; z < G; ++z)
+                                    for (int z = 0; z < G; ++z) tmem_ld(ta + g * NTOK + n + 16 * z, v[z]);
+                                    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-                                    for (int x = 0; x < 16; x += 2) {
-                                        uint64_t& p = acc[(n + 16 * z + x) / 2];
-                                        p = f2_fma(f2_pack(f, f),
-                                                   f2_pack(__uint_as_float(v[z][x]), __uint_as_float(v[z][x + 1])),
-                                                   p);
-                                    }
+                                    for (int z = 0; z < G; ++z)
+#pragma unroll
+                                        for (int x = 0; x < 16; x += 2) {
+                                            uint64_t& p = acc[(n + 16 * z + x) / 2];
+                                            p = f2_fma(f2_pack(f, f),
+                                                       f2_pack(__uint_as_float(v[z][x]),
+                                                               __uint_as_float(v[z][x + 1])),
+                                                       p);
+                                        }
+                                }
                             }
-                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(tempty + 8 * done);
+#pragma unroll
+                    for (int y = 0; y < PS; ++y) read_scales(s + TW_AHEAD * PS + y, sc[z0][y]);
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(tempty + 8 * done);
-#pragma unroll
-                for (int z = 0; z + PS < TW_AHEAD; ++z)
-#pragma unroll
-                    for (int h = 0; h < SG; ++h) sc[z][h] = sc[z + PS][h];
-#pragma unroll
-                for (int z = 0; z < PS; ++z) read_scales(s + TW_AHEAD + z, sc[TW_AHEAD - PS + z]);
             }
             // the tile's sums of this CTA's K, then of the cluster's, NR tokens at a
             // time; this CTA writes its share of each round
