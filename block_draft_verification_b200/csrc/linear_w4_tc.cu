@@ -18,9 +18,9 @@
 //
 // Tiles are taken by clusters of S CTAs that split K; the sums meet in
 // distributed shared memory in rank order: no workspace, no atomics.  S is the
-// one that leaves the SMs least idle.  Every wait is bounded (stream.cuh); on a
-// timeout a flag is set, the roles leave their loops, copies and MMAs in flight
-// are waited for (bounded) and TMEM is released.
+// one that leaves the SMs least idle.  Every wait is bounded (tw_wait); after one
+// that ran out the roles pass through their loops without waiting, a flag is set,
+// copies and MMAs in flight are waited for (bounded) and TMEM is released.
 #include <cooperative_groups.h>
 #include <cuda.h>
 
@@ -41,7 +41,9 @@ constexpr int TW_ROWS = 128;            // weight rows per tile: four units
 constexpr int TW_DEQ = 16, TW_SUM = 8;  // warps
 constexpr int TW_THREADS = 32 * (4 + TW_DEQ + TW_SUM);
 constexpr int TW_SUB = TW_ROWS * 128;   // bytes of 64 k of A
-constexpr int TW_NA = 4;                // chunks of A, and of x, in their rings
+constexpr int TW_NA = 4;                // chunks in the A ring
+// Chunks in the X ring: it covers the latency of L2 and a chunk's MMAs.
+__host__ __device__ constexpr int tw_x_stages(int n) { return n == 128 ? 5 : 8; }
 // Registers: 896 threads are launched with 72 each, 64,512; 128 x 40 + 512 x 48 +
 // 256 x 136 use all of them after the split.
 
@@ -66,7 +68,7 @@ __host__ __device__ constexpr int tw_round(int n) { return n < 64 ? n : 64; }
 // Shared memory but for the W ring: 1 KB to align the start, the A and X rings,
 // a round's sums, the barriers.
 __host__ __device__ constexpr int tw_fixed(int n) {
-    return 1024 + TW_NA * (TW_SUB + n * 128) + tw_round(n) * TW_ROWS * 4 + 512;
+    return 1024 + TW_NA * TW_SUB + tw_x_stages(n) * n * 128 + tw_round(n) * TW_ROWS * 4 + 512;
 }
 // Steps in the W ring: what is left, and no more than 12.
 __host__ __device__ constexpr int tw_w_stages(int n, int kb, int sg, int fmt) {
@@ -113,32 +115,52 @@ __device__ __forceinline__ void cluster_arrive(uint32_t bar, int rank) {
         "r"(rank)
         : "memory");
 }
-__device__ __forceinline__ bool cluster_wait(uint32_t bar, uint32_t parity) {
-    const uint64_t t0 = global_ns();
-    while (true) {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(bar), "r"(parity), "r"(SUSPEND_NS)
-            : "memory");
-        if (done) return true;
-        if (global_ns() - t0 > WAIT_NS) return false;
-    }
+// Waits, bounded: `tries` tries of up to a microsecond each; a wait that runs out
+// leaves `tries` at 1, so that everything after it passes at once and the role runs
+// to its end (with results that do not count: tw_report sets the error flag).
+// The loop is one piece of assembly without a result to branch on: the code around
+// it stays on the warp's common path, where the MMA warp's operands are uniform.
+// tried: the barrier was tested before and found done.
+constexpr uint32_t TW_TRIES = 1000000u;
+__device__ __forceinline__ void tw_wait(uint32_t bar, uint32_t parity, uint32_t& tries, bool tried = false) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+        "setp.ne.u32 q, %4, 0;\n\t@q bra DONE;\n\t"
+        "mov.u32 n, %0;\n"
+        "TRY:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "@p bra DONE;\n\t"
+        "add.u32 n, n, -1;\n\tsetp.ne.u32 q, n, 0;\n\t@q bra TRY;\n\t"
+        "mov.u32 %0, 1;\n"
+        "DONE:\n\t}"
+        : "+r"(tries)
+        : "r"(bar), "r"(parity), "r"(1000u), "r"((uint32_t)tried)
+        : "memory");
 }
-// (volatile, so after the wait for the sums; no memory clobber, so that several
-// are in flight)
-__device__ __forceinline__ float4 ld_cluster4(uint32_t addr, int rank) {
-    float4 v;
+__device__ __forceinline__ void tw_wait_cluster(uint32_t bar, uint32_t parity, uint32_t& tries) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+        "mov.u32 n, %0;\n"
+        "TRY:\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "@p bra DONE;\n\t"
+        "add.u32 n, n, -1;\n\tsetp.ne.u32 q, n, 0;\n\t@q bra TRY;\n\t"
+        "mov.u32 %0, 1;\n"
+        "DONE:\n\t}"
+        : "+r"(tries)
+        : "r"(bar), "r"(parity), "r"(1000u)
+        : "memory");
+}
+__device__ __forceinline__ void tw_report(uint32_t tries, unsigned flag) {
+    if (tries == 1u) atomicOr(&g_dev_err, flag);
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, int rank, float v) {
     asm volatile(
         "{\n\t.reg .b32 r;\n\t"
-        "mapa.shared::cluster.u32 r, %4, %5;\n\t"
-        "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [r];\n\t}"
-        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-        : "r"(addr), "r"(rank));
-    return v;
+        "mapa.shared::cluster.u32 r, %0, %1;\n\t"
+        "st.shared::cluster.f32 [r], %2;\n\t}" ::"r"(addr),
+        "r"(rank), "f"(v)
+        : "memory");
 }
 __device__ __forceinline__ void unpack4(uint2 q, float (&v)[4]) {
     v[0] = __uint_as_float(q.x << 16), v[1] = __uint_as_float(q.x & 0xFFFF0000u);
@@ -172,11 +194,6 @@ __device__ __forceinline__ void mma_commit_elect(uint32_t elected, uint32_t bar)
         "r"(elected)
         : "memory");
 }
-// The rest of a wait whose barrier was tested earlier (the answer takes about 100
-// cycles, which other work can hide).
-__device__ __forceinline__ bool mbar_settle(bool tried, uint32_t bar, uint32_t parity) {
-    return tried || mbar_wait(bar, parity);
-}
 // 32 lanes x N consecutive fp32 columns, no wait.
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
@@ -196,7 +213,7 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
     constexpr int SG = G32 ? 2 : 1;
     constexpr int SB = w4_scale_bytes(FMT), LB = SB / 8;
     constexpr int STEP = KB * W4_CHUNK_BYTES + SG * SB;
-    constexpr int NA = TW_NA, NW = tw_w_stages(NTOK, KB, SG, FMT);
+    constexpr int NA = TW_NA, NX = tw_x_stages(NTOK), NW = tw_w_stages(NTOK, KB, SG, FMT);
     constexpr int WST = tw_w_stage(KB, SG, FMT);
     constexpr int XSUB = NTOK * 128;       // bytes of 64 k of x
     constexpr int NC = NTOK / 2;           // columns per summing warp
@@ -208,13 +225,10 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sa = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t* sx = sa + NA * TW_SUB;
-    float* sp = (float*)(sx + NA * XSUB);  // [token][row] sums of a round
+    float* sp = (float*)(sx + NX * XSUB);  // [token][row] sums of a round
     uint8_t* sw = (uint8_t*)sp + NR * TW_ROWS * 4;
     uint64_t* bars = (uint64_t*)(sw + NW * WST);
-    uint32_t* s_tmem = (uint32_t*)(bars + 48);
-    // a summing warp gave up before a tile's first, second barrier: each is set on
-    // one side of a barrier and read on the other, so all eight leave together
-    volatile int* s_fail = (volatile int*)(s_tmem + 1);
+    uint32_t* s_tmem = (uint32_t*)(bars + 56);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = blockIdx.x % a.S, cl = blockIdx.x / a.S;
@@ -222,10 +236,10 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
     const int nst = (int)((int64_t)a.steps * (rank + 1) / a.S) - k0;
 
     const uint32_t wfull = smem_u32(bars), wempty = wfull + 8 * NW, full = wempty + 8 * NW,
-                   empty = full + 8 * NA, tfull = empty + 8 * NA, tempty = tfull + 8 * NB,
+                   empty = full + 8 * NA, xfull = empty + 8 * NA, xempty = xfull + 8 * NX,
+                   tfull = xempty + 8 * NX, tempty = tfull + 8 * NB,
                    mdone = tempty + 8 * NB, pready = mdone + 8, pfree = pready + 8;
-    // full: a chunk's A tile (one arrival per code warp) and x (one, and its bytes)
-    static_assert(2 * NW + 2 * NA + 2 * NB + 3 <= 48, "barriers");
+    static_assert(2 * NW + 2 * NA + 2 * NX + 2 * NB + 3 <= 56, "barriers");
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NW; ++i) {
@@ -233,8 +247,12 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
             mbar_init(wempty + 8 * i, 4 * KB);
         }
         for (int i = 0; i < NA; ++i) {
-            mbar_init(full + 8 * i, 4 + 1);
+            mbar_init(full + 8 * i, 4);
             mbar_init(empty + 8 * i, 1);
+        }
+        for (int i = 0; i < NX; ++i) {
+            mbar_init(xfull + 8 * i, 1);
+            mbar_init(xempty + 8 * i, 1);
         }
         for (int i = 0; i < NB; ++i) {
             mbar_init(tfull + 8 * i, 1);
@@ -244,7 +262,6 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
         mbar_init(pready, (uint32_t)a.S);
         mbar_init(pfree, (uint32_t)a.S);
         mbar_fence_init();
-        s_fail[0] = s_fail[1] = 0;
     }
     constexpr uint32_t NCOLS = NB * 2 * NTOK;
     if (warp == 1) {
@@ -261,6 +278,7 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
 
+    uint32_t tries = TW_TRIES;
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 0 && lane == 0) {
@@ -268,19 +286,14 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
             // before their copy, four at a time, so that the ring need only cover its
             // latency, not DRAM's
             int i = 0;
-            bool ok = true;
-            for (int64_t tile = cl; tile < a.tiles && ok; tile += a.C) {
+            for (int64_t tile = cl; tile < a.tiles; tile += a.C) {
                 const uint8_t* src = a.packed + w4_block(tile / a.tt * 4, a.steps, k0, STEP);
                 const int64_t next = tile + a.C;
                 const uint8_t* src1 =
                     a.packed + w4_block((next < a.tiles ? next : tile) / a.tt * 4, a.steps, k0, STEP);
                 for (int s = 0; s < nst; ++s, ++i) {
                     const int w = i % NW;
-                    if (i >= NW && !mbar_wait(wempty + 8 * w, (i / NW - 1) & 1)) {
-                        atomicOr(&g_dev_err, ERR_PRODUCER);
-                        ok = false;
-                        break;
-                    }
+                    if (i >= NW) tw_wait(wempty + 8 * w, (i / NW - 1) & 1, tries);
                     bulk_g2s(smem_u32(sw + w * WST), src + (int64_t)s * WST, WST, wfull + 8 * w);
                     if (s % 4 == 3 && i >= NW - 1) {
                         // steps s + TW_PREFETCH .. of this tile or, past its end, of the next
@@ -293,58 +306,58 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
                 }
             }
             // the last copies have landed before the CTA may leave
-            for (int q = i > NW ? i - NW : 0; q < i; ++q)
-                if (!mbar_wait(wfull + 8 * (q % NW), (q / NW) & 1)) atomicOr(&g_dev_err, ERR_DRAIN);
+            for (int q = i > NW ? i - NW : 0; q < i; ++q) tw_wait(wfull + 8 * (q % NW), (q / NW) & 1, tries);
+            tw_report(tries, ERR_PRODUCER);
         } else if (warp == 2 && lane == 0) {
             // ---------------- x
             int ci = 0;
-            bool ok = true;
-            for (int64_t tile = cl; tile < a.tiles && ok; tile += a.C) {
+            for (int64_t tile = cl; tile < a.tiles; tile += a.C) {
                 const int tok0 = (int)(tile % a.tt) * NTOK;
                 for (int s = 0; s < nst * KB; ++s, ++ci) {
-                    const int x = ci % NA;
-                    if (ci >= NA && !mbar_wait(empty + 8 * x, (ci / NA - 1) & 1)) {
-                        atomicOr(&g_dev_err, ERR_PRODUCER);
-                        ok = false;
-                        break;
-                    }
-                    mbar_expect_tx(full + 8 * x, (uint32_t)XSUB);
+                    const int x = ci % NX;
+                    if (ci >= NX) tw_wait(xempty + 8 * x, (ci / NX - 1) & 1, tries);
+                    mbar_expect_tx(xfull + 8 * x, (uint32_t)XSUB);
                     tw_load_x(smem_u32(sx + x * XSUB), &map_x, (k0 * KB + s) * W4_CHUNK, tok0,
-                              full + 8 * x);
+                              xfull + 8 * x);
                 }
             }
-            for (int q = ci > NA ? ci - NA : 0; q < ci; ++q)
-                if (!mbar_wait(full + 8 * (q % NA), (q / NA) & 1)) atomicOr(&g_dev_err, ERR_DRAIN);
+            for (int q = ci > NX ? ci - NX : 0; q < ci; ++q) tw_wait(xfull + 8 * (q % NX), (q / NX) & 1, tries);
+            tw_report(tries, ERR_PRODUCER);
         } else if (warp == 1) {
             // ---------------- MMA issuer: the whole warp waits, one lane issues
             const uint32_t elected = elect_lane();
-            int st = 0, pb = 0;
-            uint32_t par = 0, tpar = 1;  // phases of the operand ring and (waited for) of TMEM
-            bool ok = true, tried = false;
-            for (int64_t tile = cl; tile < a.tiles && ok; tile += a.C) {
+            int st = 0, sx_at = 0, pb = 0;
+            uint32_t par = 0, xpar = 0, tpar = 1;  // phases of the rings and (waited for) of TMEM
+            bool tried = false, xtried = false;
+            for (int64_t tile = cl; tile < a.tiles; tile += a.C) {
                 const int64_t left = a.tokens - (tile % a.tt) * NTOK;
                 const uint32_t idesc =
                     instr_desc(TW_ROWS, (int)min((int64_t)NTOK, (left + 15) / 16 * 16));
-                for (int s = 0; s < nst && ok; ++s) {
+                for (int s = 0; s < nst; ++s) {
                     // a pair of groups: two steps, or a step of two groups; its
                     // accumulators have been read (their first use: the phase before
                     // the first counts as done)
                     const bool opens = SG == 2 || s % 2 == 0, closes = SG == 2 || s % 2 == 1 || s + 1 == nst;
-                    if (opens) ok = mbar_wait(tempty + 8 * pb, tpar);
+                    if (opens) tw_wait(tempty + 8 * pb, tpar, tries);
                     const uint32_t d0 = tmem + (uint32_t)((2 * pb + (opens ? 0 : 1)) * NTOK);
 #pragma unroll
                     for (int c = 0; c < KB; ++c) {
-                        ok = ok && mbar_settle(tried, full + 8 * st, par);
-                        if (!ok) break;
+                        tw_wait(full + 8 * st, par, tries, tried);
+                        tw_wait(xfull + 8 * sx_at, xpar, tries, xtried);
                         tc_fence_after();
                         const uint64_t ao = smem_desc(smem_u32(sa + st * TW_SUB));
-                        const uint64_t xo = smem_desc(smem_u32(sx + st * XSUB));
-                        const uint32_t done = empty + 8 * st;
+                        const uint64_t xo = smem_desc(smem_u32(sx + sx_at * XSUB));
+                        const uint32_t done = empty + 8 * st, xdone = xempty + 8 * sx_at;
                         if (++st == NA) {
                             st = 0;
                             par ^= 1u;
                         }
+                        if (++sx_at == NX) {
+                            sx_at = 0;
+                            xpar ^= 1u;
+                        }
                         tried = mbar_test(full + 8 * st, par);
+                        xtried = mbar_test(xfull + 8 * sx_at, xpar);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
                             const bool first = SG == 2 ? kk % 2 == 0 : kk == 0 && c == 0;
@@ -352,15 +365,16 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
                                            idesc, first ? 0u : 1u);
                         }
                         mma_commit_elect(elected, done);
+                        mma_commit_elect(elected, xdone);
                     }
-                    if (ok && closes) {
+                    if (closes) {
                         mma_commit_elect(elected, tfull + 8 * pb);
                         pb ^= 1;
                         if (pb == 0) tpar ^= 1u;
                     }
                 }
             }
-            if (!ok && lane == 0) atomicOr(&g_dev_err, ERR_MMA);
+            if (lane == 0) tw_report(tries, ERR_MMA);
             mma_commit_elect(elected, mdone);  // fires when every MMA issued has completed
         }
     } else if (warp < 4 + TW_DEQ) {
@@ -389,10 +403,8 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
         static_assert(KB == 2 ? NW >= 4 : NW >= 8, "the phase before is complete");
         bool ready = false;
         for (int k = 0; k < left; ++k) {
-            if (!mbar_settle(ready, wfull + 8 * w, wpar) || !mbar_wait(empty + 8 * grp, apar)) {
-                if (lane == 0) atomicOr(&g_dev_err, ERR_EPILOGUE);
-                break;
-            }
+            tw_wait(wfull + 8 * w, wpar, tries, ready);
+            tw_wait(empty + 8 * grp, apar, tries);
             apar ^= 1u;
             const uint32_t wo = (uint32_t)(w * WST), wdone = wempty + 8 * w;
             const uint4 v[2] = {lds128(src + wo), lds128(src + wo + 512)};
@@ -430,6 +442,7 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
                 mbar_arrive(wdone);
             }
         }
+        if (lane == 0) tw_report(tries, ERR_EPILOGUE);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
         // ---------------- scaling and sums
@@ -440,7 +453,7 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
         if (a.S > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
         int round = 0, pb = 0;
         uint32_t tpar = 0;
-        bool ok = true, tried = false;
+        bool tried = false;
         for (int64_t tile = cl; tile < a.tiles; tile += a.C) {
             const int rt = (int)(tile / a.tt);
             const int tok0 = (int)(tile - (int64_t)rt * a.tt) * NTOK;
@@ -470,13 +483,12 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
             for (int n = 0; n < NC / 2; ++n) acc[n] = 0;
             // (a register that a load is still to fill is not moved: the pairs take the
             // scale registers in turn)
-            for (int s0 = 0; s0 < nst && ok; s0 += TW_AHEAD * PS) {
+            for (int s0 = 0; s0 < nst; s0 += TW_AHEAD * PS) {
 #pragma unroll
                 for (int z0 = 0; z0 < TW_AHEAD; ++z0) {
                     const int s = s0 + z0 * PS;
                     if (s >= nst) break;
-                    ok = mbar_settle(tried, tfull + 8 * pb, tpar);
-                    if (!ok) break;
+                    tw_wait(tfull + 8 * pb, tpar, tries, tried);
                     tc_fence_after();
                     const int done = pb;
                     pb ^= 1;
@@ -515,126 +527,111 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
                     for (int y = 0; y < PS; ++y) read_scales(s + TW_AHEAD * PS + y, sc[z0][y]);
                 }
             }
-            // the tile's sums of this CTA's K, then of the cluster's, NR tokens at a
-            // time; this CTA writes its share of each round
-            const int share = NR / a.S;
+            // The tile's end: the sums of this CTA's K go to the CTAs that write them,
+            // NR tokens at a time (NR / 2 of either half of the columns), each CTA a
+            // share of them; its shared memory holds [rank of origin][token][row].
+            constexpr int CPR = NR / 2;
+            const int share = NR / a.S, lsh = 31 - __clz(share);
             const uint32_t spu = smem_u32(sp);
-            // four rows of M items' tokens: every item's part from one CTA before the
-            // next CTA's, so that the reads are in flight together
-            auto sum4 = [&](auto& v, int row, int t, int dt, int last) {
-                constexpr int M = sizeof(v) / sizeof(v[0]);
+            auto token_of = [&](int t, int rd) { return (t / CPR) * NC + rd * CPR + t % CPR; };
 #pragma unroll
-                for (int z = 0; z < M; ++z) v[z] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                for (int k = 0; k < a.S; ++k) {
-                    float4 f[M];
+            for (int rd = 0; rd < NC / CPR; ++rd) {
+                if (rd * CPR >= ntok) break;  // the same in every CTA of the cluster
+                if (a.S > 1 && round > 0) tw_wait_cluster(pfree, (round - 1) & 1, tries);
+                {
+                    const uint32_t own = spu + 4 * (((rank << lsh) * TW_ROWS) + 32 * q + lane);
 #pragma unroll
-                    for (int z = 0; z < M; ++z)
-                        f[z] = ld_cluster4(spu + 4 * (min(t + dt * z, last) * TW_ROWS + row), k);
-#pragma unroll
-                    for (int z = 0; z < M; ++z)
-                        v[z].x += f[z].x, v[z].y += f[z].y, v[z].z += f[z].z, v[z].w += f[z].w;
-                }
-            };
-            const int rounds = (ntok + NR - 1) / NR;  // the same in every CTA of the cluster
-            for (int rd = 0; rd < rounds; ++rd, ++round) {
-                const int t0 = share * rank, t1 = min(t0 + share, ntok - rd * NR);
-                const int tokr = tok0 + rd * NR;  // the round's first token
-                if (ok && a.S > 1 && round > 0) ok = cluster_wait(pfree, (round - 1) & 1);
-                if (!ok) {
-                    atomicOr(&g_dev_err, (unsigned)ERR_EPILOGUE);
-                    s_fail[0] = 1;
-                } else if (NR == NTOK || half == rd) {
-                    float* d = sp + (NR == NTOK ? half * NC : 0) * TW_ROWS + 32 * q + lane;
-#pragma unroll
-                    for (int n = 0; n < NC; n += 2) {
-                        d[n * TW_ROWS] = f2_lo(acc[n / 2]);
-                        d[(n + 1) * TW_ROWS] = f2_hi(acc[n / 2]);
+                    for (int n = 0; n < CPR; ++n) {
+                        const int t = half * CPR + n;
+                        const uint64_t pr = acc[(rd * CPR + n) / 2];
+                        const float v = (n & 1) ? f2_hi(pr) : f2_lo(pr);
+                        const uint32_t o = own + 4 * ((t & (share - 1)) * TW_ROWS);
+                        if (a.S == 1)
+                            asm volatile("st.shared.f32 [%0], %1;" ::"r"(o), "f"(v) : "memory");
+                        else
+                            st_cluster(o, t >> lsh, v);
                     }
                 }
                 asm volatile("bar.sync 1, 256;" ::: "memory");
-                if (s_fail[0]) break;
                 if (a.S > 1 && e < a.S) cluster_arrive(pready, e);
-                auto joined = [&]() {
-                    if (a.S > 1) ok = cluster_wait(pready, round & 1);
-                    if (!ok) {
-                        atomicOr(&g_dev_err, (unsigned)ERR_EPILOGUE);
-                        s_fail[1] = 1;
+                // x of the conv's tokens is on its way meanwhile
+                const int c4 = (e & 15) * 4, ch = rt * 64 + c4;
+                uint2 xc[2], xp[2];
+                auto load_x = [&](int tl) {
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        const int t = token_of(rank * share + min(tl + 16 * z, share - 1), rd);
+                        const int tok = tok0 + min(t, ntok - 1), sq = tok / a.T;
+                        const __nv_bfloat16* x = a.x + tok * a.ld + ch;
+                        xc[z] = __ldg((const uint2*)x);
+                        xp[z] = __ldg((const uint2*)(tok == sq * a.T ? a.x_prev + sq * a.ld + ch : x - a.ld));
                     }
+                };
+                if (a.x_prev) load_x(e >> 4);
+                if (a.S > 1) tw_wait_cluster(pready, round & 1, tries);
+                auto sum4 = [&](int row, int tl) {  // four rows of a token, over the cluster
+                    const float4* p = (const float4*)(sp + tl * TW_ROWS + row);
+                    float4 v = p[0];
+                    for (int k = 1; k < a.S; ++k) {
+                        const float4 f = p[k * share * (TW_ROWS / 4)];
+                        v.x += f.x, v.y += f.y, v.z += f.z, v.w += f.w;
+                    }
+                    return v;
                 };
                 if (!a.x_prev) {
                     const int row = (e & 31) * 4;
                     const int64_t n = (int64_t)rt * TW_ROWS + row;
-                    const int64_t o0 = tokr * a.ld + n;
-                    joined();
-                    for (int t = t0 + (e >> 5); t < t1 && ok; t += 32) {
-                        float4 v[4];
-                        sum4(v, row, t, 8, t1 - 1);
+#pragma unroll 2
+                    for (int tl = e >> 5; tl < share; tl += 8) {
+                        const int t = token_of(rank * share + tl, rd);
+                        if (t >= ntok) continue;
+                        const float4 v = sum4(row, tl);
+                        const int64_t o = (tok0 + t) * a.ld + n;
+                        const float w4[4] = {v.x, v.y, v.z, v.w};
+                        if (a.y_vec && n + 4 <= a.n_rows) {
+                            if (a.y_bf16)
+                                *(uint2*)((__nv_bfloat16*)a.y + o) = pack4(w4);
+                            else
+                                *(float4*)((float*)a.y + o) = v;
+                        } else {
 #pragma unroll
-                        for (int z = 0; z < 4; ++z) {
-                            if (t + 8 * z >= t1) break;
-                            const int64_t o = o0 + (t + 8 * z) * a.ld;
-                            const float w4[4] = {v[z].x, v[z].y, v[z].z, v[z].w};
-                            if (a.y_vec && n + 4 <= a.n_rows) {
-                                if (a.y_bf16)
-                                    *(uint2*)((__nv_bfloat16*)a.y + o) = pack4(w4);
-                                else
-                                    *(float4*)((float*)a.y + o) = v[z];
-                            } else {
-#pragma unroll
-                                for (int p = 0; p < 4; ++p)
-                                    if (n + p < a.n_rows) {
-                                        if (a.y_bf16)
-                                            ((__nv_bfloat16*)a.y)[o + p] = __float2bfloat16_rn(w4[p]);
-                                        else
-                                            ((float*)a.y)[o + p] = w4[p];
-                                    }
-                            }
+                            for (int p = 0; p < 4; ++p)
+                                if (n + p < a.n_rows) {
+                                    if (a.y_bf16)
+                                        ((__nv_bfloat16*)a.y)[o + p] = __float2bfloat16_rn(w4[p]);
+                                    else
+                                        ((float*)a.y)[o + p] = w4[p];
+                                }
                         }
                     }
                 } else {
                     // a and b of a channel: rows 8 apart (w4_pack, taps); H is a multiple
                     // of 64, so a tile's 64 channels are all there
-                    const int c4 = (e & 15) * 4, row = (c4 >> 3) * 16 + (c4 & 7);
-                    const int ch = rt * 64 + c4;
-                    uint2 xc[2], xp[2];
-                    auto load_x = [&](int t) {
+                    const int row = (c4 >> 3) * 16 + (c4 & 7);
+                    for (int tl = e >> 4; tl < share; tl += 32) {
 #pragma unroll
                         for (int z = 0; z < 2; ++z) {
-                            const int tok = tokr + min(t + 16 * z, t1 - 1), sq = tok / a.T;
-                            const __nv_bfloat16* x = a.x + tok * a.ld + ch;
-                            xc[z] = __ldg((const uint2*)x);
-                            xp[z] = __ldg((const uint2*)(tok == sq * a.T ? a.x_prev + sq * a.ld + ch : x - a.ld));
-                        }
-                    };
-                    int t = t0 + (e >> 4);
-                    if (t < t1) load_x(t);  // on its way while the cluster's sums come in
-                    joined();
-                    for (; t < t1 && ok; t += 32) {
-                        float4 av[2], bv[2];
-                        sum4(av, row, t, 16, t1 - 1);
-                        sum4(bv, row + 8, t, 16, t1 - 1);
-#pragma unroll
-                        for (int z = 0; z < 2; ++z) {
-                            if (t + 16 * z >= t1) break;
-                            const float a4[4] = {av[z].x, av[z].y, av[z].z, av[z].w};
-                            const float b4[4] = {bv[z].x, bv[z].y, bv[z].z, bv[z].w};
+                            const int tz = tl + 16 * z, t = token_of(rank * share + tz, rd);
+                            if (tz >= share || t >= ntok) continue;
+                            const float4 av = sum4(row, tz), bv = sum4(row + 8, tz);
+                            const float a4[4] = {av.x, av.y, av.z, av.w}, b4[4] = {bv.x, bv.y, bv.z, bv.w};
                             float c[4], p[4];
                             unpack4(xc[z], c);
                             unpack4(xp[z], p);
 #pragma unroll
                             for (int q2 = 0; q2 < 4; ++q2)
                                 c[q2] = fmaf(b4[q2], p[q2], fmaf(a4[q2], c[q2], c[q2]));
-                            *(uint2*)((__nv_bfloat16*)a.y + (int64_t)(tokr + t + 16 * z) * a.ld + ch) = pack4(c);
+                            *(uint2*)((__nv_bfloat16*)a.y + (int64_t)(tok0 + t) * a.ld + ch) = pack4(c);
                         }
-                        if (t + 32 < t1) load_x(t + 32);
+                        if (tl + 32 < share) load_x(tl + 32);
                     }
                 }
                 asm volatile("bar.sync 1, 256;" ::: "memory");
-                if (s_fail[1]) break;
                 if (a.S > 1 && e < a.S) cluster_arrive(pfree, e);
+                ++round;
             }
-            if (s_fail[0] || s_fail[1]) break;
         }
+        if (lane == 0) tw_report(tries, ERR_EPILOGUE);
     }
     if (a.S > 1 && warp < 4 + TW_DEQ) {
         __syncwarp();
@@ -642,7 +639,8 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
     }
     __syncthreads();
     if (warp == 1) {
-        if (!mbar_wait(mdone, 0) && lane == 0) atomicOr(&g_dev_err, ERR_DRAIN);
+        tw_wait(mdone, 0, tries);
+        if (lane == 0) tw_report(tries, ERR_DRAIN);
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(NCOLS));
     }
