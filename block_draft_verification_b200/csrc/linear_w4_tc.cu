@@ -154,14 +154,6 @@ __device__ __forceinline__ void tw_wait_cluster(uint32_t bar, uint32_t parity, u
 __device__ __forceinline__ void tw_report(uint32_t tries, unsigned flag) {
     if (tries == 1u) atomicOr(&g_dev_err, flag);
 }
-__device__ __forceinline__ void st_cluster(uint32_t addr, int rank, float v) {
-    asm volatile(
-        "{\n\t.reg .b32 r;\n\t"
-        "mapa.shared::cluster.u32 r, %0, %1;\n\t"
-        "st.shared::cluster.f32 [r], %2;\n\t}" ::"r"(addr),
-        "r"(rank), "f"(v)
-        : "memory");
-}
 __device__ __forceinline__ void unpack4(uint2 q, float (&v)[4]) {
     v[0] = __uint_as_float(q.x << 16), v[1] = __uint_as_float(q.x & 0xFFFF0000u);
     v[2] = __uint_as_float(q.y << 16), v[3] = __uint_as_float(q.y & 0xFFFF0000u);
@@ -203,6 +195,141 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
           "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
           "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
+}
+
+// What a summing thread needs at a tile's end.
+struct TwEnd {
+    const W4TcArgs* a;
+    float* sp;            // [rank of origin][token of the share][row]
+    uint32_t tries;
+    int rank, rt, tok0, ntok, e, half, q;
+    uint32_t pready, pfree;
+    int round;            // rounds before this tile's
+};
+
+// The sums of this CTA's K go to the CTAs of the cluster that write them, tw_round
+// tokens at a time (half of them of either half of the columns), each CTA a share of
+// them; then they are added in rank order and written.
+template <int NTOK, int S>
+__device__ __forceinline__ uint32_t tw_tile_end(const TwEnd& f, const uint64_t (&acc)[NTOK / 4]) {
+    constexpr int NC = NTOK / 2, NR = tw_round(NTOK), CPR = NR / 2, SHARE = NR / S;
+    const W4TcArgs& a = *f.a;
+    uint32_t tries = f.tries;
+    const int e = f.e, lane = e & 31;
+    const uint32_t spu = smem_u32(f.sp);
+    auto token_of = [](int t, int rd) { return (t / CPR) * NC + rd * CPR + t % CPR; };
+#pragma unroll
+    for (int rd = 0; rd < NC / CPR; ++rd) {
+        const int round = f.round + rd;
+        if (rd * CPR >= f.ntok) break;  // the same in every CTA of the cluster
+        if (S > 1 && round > 0) tw_wait_cluster(f.pfree, (round - 1) & 1, tries);
+        const uint32_t own = spu + 4 * (f.rank * SHARE * TW_ROWS + 32 * f.q + lane);
+        if constexpr (S == 1) {
+            const uint32_t o = own + 4 * f.half * CPR * TW_ROWS;
+#pragma unroll
+            for (int n = 0; n < CPR; ++n) {
+                const uint64_t pr = acc[(rd * CPR + n) / 2];
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(o + 4 * n * TW_ROWS),
+                             "f"((n & 1) ? f2_hi(pr) : f2_lo(pr))
+                             : "memory");
+            }
+        } else {
+            // this half's CPR tokens are CPR / SHARE whole shares (S = 2: one)
+            static_assert(CPR % SHARE == 0, "a half of a round is whole shares");
+#pragma unroll
+            for (int b = 0; b < CPR / SHARE; ++b) {
+                uint32_t o;
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                             : "=r"(o)
+                             : "r"(own), "r"(f.half * (CPR / SHARE) + b));
+#pragma unroll
+                for (int n = 0; n < SHARE; ++n) {
+                    const int i = rd * CPR + b * SHARE + n;
+                    const uint64_t pr = acc[i / 2];
+                    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(o + 4 * n * TW_ROWS),
+                                 "f"((i & 1) ? f2_hi(pr) : f2_lo(pr))
+                                 : "memory");
+                }
+            }
+        }
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (S > 1 && e < S) cluster_arrive(f.pready, e);
+        auto sum4 = [&](int row, int tl) {  // four rows of a token, over the cluster
+            const uint32_t p = spu + 4 * (tl * TW_ROWS + row);
+            float4 v[S];
+#pragma unroll
+            for (int k = 0; k < S; ++k) {
+                const uint4 u = lds128(p + 4 * k * SHARE * TW_ROWS);
+                v[k] = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z),
+                                   __uint_as_float(u.w));
+            }
+#pragma unroll
+            for (int k = 1; k < S; ++k)
+                v[0].x += v[k].x, v[0].y += v[k].y, v[0].z += v[k].z, v[0].w += v[k].w;
+            return v[0];
+        };
+        if (!a.x_prev) {
+            const int row = (e & 31) * 4;
+            const int64_t n = (int64_t)f.rt * TW_ROWS + row;
+            const bool vec = a.y_vec && n + 4 <= a.n_rows;
+            if (S > 1) tw_wait_cluster(f.pready, round & 1, tries);
+#pragma unroll
+            for (int i = 0; i < (SHARE + 7) / 8; ++i) {
+                const int tl = (e >> 5) + 8 * i, t = token_of(f.rank * SHARE + tl, rd);
+                if ((SHARE % 8 != 0 && tl >= SHARE) || t >= f.ntok) continue;
+                const float4 v = sum4(row, tl);
+                const int64_t o = (f.tok0 + t) * a.ld + n;
+                const float w4[4] = {v.x, v.y, v.z, v.w};
+                if (vec) {
+                    if (a.y_bf16)
+                        *(uint2*)((__nv_bfloat16*)a.y + o) = pack4(w4);
+                    else
+                        *(float4*)((float*)a.y + o) = v;
+                } else {
+#pragma unroll
+                    for (int p = 0; p < 4; ++p)
+                        if (n + p < a.n_rows) {
+                            if (a.y_bf16)
+                                ((__nv_bfloat16*)a.y)[o + p] = __float2bfloat16_rn(w4[p]);
+                            else
+                                ((float*)a.y)[o + p] = w4[p];
+                        }
+                }
+            }
+        } else {
+            // a and b of a channel: rows 8 apart (w4_pack, taps); H is a multiple of 64,
+            // so a tile's 64 channels are all there.  x is on its way while the
+            // cluster's sums come in.
+            const int c4 = (e & 15) * 4, ch = f.rt * 64 + c4, row = (c4 >> 3) * 16 + (c4 & 7);
+            constexpr int M = (SHARE + 15) / 16;  // items of a thread
+            uint2 xc[M], xp[M];
+#pragma unroll
+            for (int i = 0; i < M; ++i) {
+                const int t = token_of(f.rank * SHARE + (e >> 4) + 16 * i, rd);
+                const int tok = f.tok0 + min(t, f.ntok - 1), sq = tok / a.T;
+                const __nv_bfloat16* x = a.x + tok * a.ld + ch;
+                xc[i] = __ldg((const uint2*)x);
+                xp[i] = __ldg((const uint2*)(tok == sq * a.T ? a.x_prev + sq * a.ld + ch : x - a.ld));
+            }
+            if (S > 1) tw_wait_cluster(f.pready, round & 1, tries);
+#pragma unroll
+            for (int i = 0; i < M; ++i) {
+                const int tl = (e >> 4) + 16 * i, t = token_of(f.rank * SHARE + tl, rd);
+                if ((SHARE % 16 != 0 && tl >= SHARE) || t >= f.ntok) continue;
+                const float4 av = sum4(row, tl), bv = sum4(row + 8, tl);
+                const float a4[4] = {av.x, av.y, av.z, av.w}, b4[4] = {bv.x, bv.y, bv.z, bv.w};
+                float c[4], p[4];
+                unpack4(xc[i], c);
+                unpack4(xp[i], p);
+#pragma unroll
+                for (int z = 0; z < 4; ++z) c[z] = fmaf(b4[z], p[z], fmaf(a4[z], c[z], c[z]));
+                *(uint2*)((__nv_bfloat16*)a.y + (int64_t)(f.tok0 + t) * a.ld + ch) = pack4(c);
+            }
+        }
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (S > 1 && e < S) cluster_arrive(f.pfree, e);
+    }
+    return tries;
 }
 
 // NTOK: tokens per tile (32, 64, 128); FMT: scale format; G32: groups of 32, two
@@ -527,109 +654,18 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
                     for (int y = 0; y < PS; ++y) read_scales(s + TW_AHEAD * PS + y, sc[z0][y]);
                 }
             }
-            // The tile's end: the sums of this CTA's K go to the CTAs that write them,
-            // NR tokens at a time (NR / 2 of either half of the columns), each CTA a
-            // share of them; its shared memory holds [rank of origin][token][row].
-            constexpr int CPR = NR / 2;
-            const int share = NR / a.S, lsh = 31 - __clz(share);
-            const uint32_t spu = smem_u32(sp);
-            auto token_of = [&](int t, int rd) { return (t / CPR) * NC + rd * CPR + t % CPR; };
-#pragma unroll
-            for (int rd = 0; rd < NC / CPR; ++rd) {
-                if (rd * CPR >= ntok) break;  // the same in every CTA of the cluster
-                if (a.S > 1 && round > 0) tw_wait_cluster(pfree, (round - 1) & 1, tries);
-                {
-                    const uint32_t own = spu + 4 * (((rank << lsh) * TW_ROWS) + 32 * q + lane);
-#pragma unroll
-                    for (int n = 0; n < CPR; ++n) {
-                        const int t = half * CPR + n;
-                        const uint64_t pr = acc[(rd * CPR + n) / 2];
-                        const float v = (n & 1) ? f2_hi(pr) : f2_lo(pr);
-                        const uint32_t o = own + 4 * ((t & (share - 1)) * TW_ROWS);
-                        if (a.S == 1)
-                            asm volatile("st.shared.f32 [%0], %1;" ::"r"(o), "f"(v) : "memory");
-                        else
-                            st_cluster(o, t >> lsh, v);
-                    }
-                }
-                asm volatile("bar.sync 1, 256;" ::: "memory");
-                if (a.S > 1 && e < a.S) cluster_arrive(pready, e);
-                // x of the conv's tokens is on its way meanwhile
-                const int c4 = (e & 15) * 4, ch = rt * 64 + c4;
-                uint2 xc[2], xp[2];
-                auto load_x = [&](int tl) {
-#pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        const int t = token_of(rank * share + min(tl + 16 * z, share - 1), rd);
-                        const int tok = tok0 + min(t, ntok - 1), sq = tok / a.T;
-                        const __nv_bfloat16* x = a.x + tok * a.ld + ch;
-                        xc[z] = __ldg((const uint2*)x);
-                        xp[z] = __ldg((const uint2*)(tok == sq * a.T ? a.x_prev + sq * a.ld + ch : x - a.ld));
-                    }
-                };
-                if (a.x_prev) load_x(e >> 4);
-                if (a.S > 1) tw_wait_cluster(pready, round & 1, tries);
-                auto sum4 = [&](int row, int tl) {  // four rows of a token, over the cluster
-                    const float4* p = (const float4*)(sp + tl * TW_ROWS + row);
-                    float4 v = p[0];
-                    for (int k = 1; k < a.S; ++k) {
-                        const float4 f = p[k * share * (TW_ROWS / 4)];
-                        v.x += f.x, v.y += f.y, v.z += f.z, v.w += f.w;
-                    }
-                    return v;
-                };
-                if (!a.x_prev) {
-                    const int row = (e & 31) * 4;
-                    const int64_t n = (int64_t)rt * TW_ROWS + row;
-#pragma unroll 2
-                    for (int tl = e >> 5; tl < share; tl += 8) {
-                        const int t = token_of(rank * share + tl, rd);
-                        if (t >= ntok) continue;
-                        const float4 v = sum4(row, tl);
-                        const int64_t o = (tok0 + t) * a.ld + n;
-                        const float w4[4] = {v.x, v.y, v.z, v.w};
-                        if (a.y_vec && n + 4 <= a.n_rows) {
-                            if (a.y_bf16)
-                                *(uint2*)((__nv_bfloat16*)a.y + o) = pack4(w4);
-                            else
-                                *(float4*)((float*)a.y + o) = v;
-                        } else {
-#pragma unroll
-                            for (int p = 0; p < 4; ++p)
-                                if (n + p < a.n_rows) {
-                                    if (a.y_bf16)
-                                        ((__nv_bfloat16*)a.y)[o + p] = __float2bfloat16_rn(w4[p]);
-                                    else
-                                        ((float*)a.y)[o + p] = w4[p];
-                                }
-                        }
-                    }
-                } else {
-                    // a and b of a channel: rows 8 apart (w4_pack, taps); H is a multiple
-                    // of 64, so a tile's 64 channels are all there
-                    const int row = (c4 >> 3) * 16 + (c4 & 7);
-                    for (int tl = e >> 4; tl < share; tl += 32) {
-#pragma unroll
-                        for (int z = 0; z < 2; ++z) {
-                            const int tz = tl + 16 * z, t = token_of(rank * share + tz, rd);
-                            if (tz >= share || t >= ntok) continue;
-                            const float4 av = sum4(row, tz), bv = sum4(row + 8, tz);
-                            const float a4[4] = {av.x, av.y, av.z, av.w}, b4[4] = {bv.x, bv.y, bv.z, bv.w};
-                            float c[4], p[4];
-                            unpack4(xc[z], c);
-                            unpack4(xp[z], p);
-#pragma unroll
-                            for (int q2 = 0; q2 < 4; ++q2)
-                                c[q2] = fmaf(b4[q2], p[q2], fmaf(a4[q2], c[q2], c[q2]));
-                            *(uint2*)((__nv_bfloat16*)a.y + (int64_t)(tok0 + t) * a.ld + ch) = pack4(c);
-                        }
-                        if (tl + 32 < share) load_x(tl + 32);
-                    }
-                }
-                asm volatile("bar.sync 1, 256;" ::: "memory");
-                if (a.S > 1 && e < a.S) cluster_arrive(pfree, e);
-                ++round;
-            }
+            // The tile's end, written out for each cluster size: its loops are short and
+            // unrolled, their addresses constants.
+            const TwEnd t{&a, sp, tries, rank, rt, tok0, ntok, e, half, q, pready, pfree, round};
+            if (a.S == 1)
+                tries = tw_tile_end<NTOK, 1>(t, acc);
+            else if (a.S == 2)
+                tries = tw_tile_end<NTOK, 2>(t, acc);
+            else if (a.S == 4)
+                tries = tw_tile_end<NTOK, 4>(t, acc);
+            else
+                tries = tw_tile_end<NTOK, 8>(t, acc);
+            round += min(NTOK / NR, (ntok + NR / 2 - 1) / (NR / 2));
         }
         if (lane == 0) tw_report(tries, ERR_EPILOGUE);
     }
