@@ -75,6 +75,13 @@ __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(a));
+    return v;
+}
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -168,13 +175,13 @@ __global__ void __launch_bounds__(W4_THREADS, 1) linear_w4_kernel(const W4Args a
     const int k0 = a.steps * rank / a.S, k1 = a.steps * (rank + 1) / a.S;
     const int64_t u0 = a.units * cl / a.C, u1 = a.units * (cl + 1) / a.C;
 
-    // shared memory: the warps' rings, x [chunk][half][plane][token][32 k] bf16
-    // (64-byte rows), the sums of x [step][group of the step][8 NT tokens]
+    // shared memory: the warps' rings, x [chunk][half][plane][8 NT tokens][32 k]
+    // bf16 (64-byte rows), the sums of x [step][group of the step][8 NT tokens]
     // (OFFS), then the partial sums [unit of the batch][slot][NT * 8][32 lanes]
     // fp32 and the units' slot counts
-    const int xrow = nt * 64, xchunk = 2 * NP * xrow;
-    uint8_t* ring = smem + warp * (D * STAGE);
-    const uint32_t ring_u = smem_u32(ring) + lane * 16, ring_s = smem_u32(ring) + KB * W4_CHUNK_BYTES + lane * LB;
+    constexpr int XROW = NT * 8 * 64, XSTEP = KB * 2 * NP * XROW;
+    const uint32_t ring = smem_u32(smem + warp * (D * STAGE));
+    const uint32_t ring_u = ring + lane * 16, ring_s = ring + KB * W4_CHUNK_BYTES + lane * LB;
     uint8_t* xs = smem + a.x_off;
     float* xsum = (float*)(smem + a.xsum_off);
     float* part = (float*)(smem + a.part_off);
@@ -191,17 +198,18 @@ __global__ void __launch_bounds__(W4_THREADS, 1) linear_w4_kernel(const W4Args a
 
     // The run at hand, of batch ub and phase ph: its items are cu, cc (unit and
     // step) onward; `left` of them are not yet requested.
-    int c0 = 0, nc = 0, n = 0, cu = 0, cc = 0, len = 0, left = 0, lc = 0, st_load = 0, st_read = 0;
+    int c0 = 0, nc = 0, n = 0, cu = 0, cc = 0, len = 0, left = 0, lc = 0;
     int64_t lu = 0;  // unit and step (of the run's part of K) of the next request
     const uint8_t* lw = nullptr;
-    auto request = [&]() {  // the next step into the ring (an empty group at the run's end)
+    // the next step into a stage of the ring (an empty group at the run's end)
+    auto request = [&](int stage) {
         if (left > 0) {
             --left;
-            const uint32_t dst = ring_u + st_load * STAGE;
+            const uint32_t dst = ring_u + stage * STAGE;
             const uint8_t* src = lw + lane * 16;
 #pragma unroll
             for (int q = 0; q < 2 * KB; ++q) cp_async16(dst + q * 512, src + q * 512);
-            const uint32_t dsc = ring_s + st_load * STAGE;
+            const uint32_t dsc = ring_s + stage * STAGE;
             const uint8_t* ssc = lw + KB * W4_CHUNK_BYTES + (lane >> 2) * LB;
 #pragma unroll
             for (int h = 0; h < SG; ++h) {
@@ -213,7 +221,6 @@ __global__ void __launch_bounds__(W4_THREADS, 1) linear_w4_kernel(const W4Args a
                         cp_async16(dsc + h * 32 * LB + 16 * q, ssc + h * 8 * LB + 16 * q);
                 }
             }
-            st_load = st_load + 1 == D ? 0 : st_load + 1;
             lw += 4 * STEP;
             if (++lc == nc) {
                 lc = 0;
@@ -235,9 +242,8 @@ __global__ void __launch_bounds__(W4_THREADS, 1) linear_w4_kernel(const W4Args a
         lc = cc = i0 - cu * nc;
         lu = ub + cu;
         lw = a.packed + w4_block(lu, a.steps, c0 + cc, STEP);
-        st_load = st_read = 0;
 #pragma unroll
-        for (int d = 0; d < D - 1; ++d) request();
+        for (int d = 0; d < D - 1; ++d) request(d);
     };
 
     start(u0, 0);
@@ -256,7 +262,7 @@ __global__ void __launch_bounds__(W4_THREADS, 1) linear_w4_kernel(const W4Args a
                     load_x8<XT, NP>(row, (int64_t)(2 * KB * c0 + ch) * 32 + 8 * c8, a.K, a.x_vec != 0, v);
 #pragma unroll
                     for (int p = 0; p < NP; ++p)
-                        *(uint4*)(xs + (size_t)(ch * NP + p) * xrow + t * 64 + c8 * 16) = v[p];
+                        *(uint4*)(xs + (size_t)(ch * NP + p) * XROW + t * 64 + c8 * 16) = v[p];
                 }
                 if (phases > 1 && ph == 0)
                     for (int i = threadIdx.x; i < nu * a.slots * PU; i += W4_THREADS) part[i] = 0.0f;
@@ -273,7 +279,7 @@ __global__ void __launch_bounds__(W4_THREADS, 1) linear_w4_kernel(const W4Args a
                         if (t < nt) {
 #pragma unroll
                             for (int h = 0; h < HALVES; ++h) {
-                                const uint4 q = *(const uint4*)(xs + (size_t)(pc * HALVES + h) * xrow +
+                                const uint4 q = *(const uint4*)(xs + (size_t)(pc * HALVES + h) * XROW +
                                                                 t * 64 + c8 * 16);
                                 const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -301,23 +307,26 @@ __global__ void __launch_bounds__(W4_THREADS, 1) linear_w4_kernel(const W4Args a
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) acc[b][t][j] = 0.0f;
-            for (int i = 0; i < len; ++i) {
+            const uint32_t xs_u = smem_u32(xs);
+            uint32_t xc = xs_u + cc * XSTEP;
+            const float* xq = xsum + (size_t)cc * SG * 8 * NT + 2 * (lane & 3);
+            for (int i0 = 0; i0 < len; i0 += D) {
+#pragma unroll
+              for (int d = 0; d < D; ++d) {  // the ring's stages in turn
+                const int i = i0 + d;
+                if (i >= len) break;
                 cp_async_wait<D - 2>();
-                const uint8_t* sp = ring + st_read * STAGE;
-                st_read = st_read + 1 == D ? 0 : st_read + 1;
-                request();  // into the stage that the step before this one has left
+                request((d + D - 1) % D);  // the stage that the step before this one has left
                 W4Scale<FMT> w4s[SG];
 #pragma unroll
-                for (int h = 0; h < SG; ++h) w4s[h].load(sp + KB * W4_CHUNK_BYTES + (h * 32 + lane) * LB);
+                for (int h = 0; h < SG; ++h) w4s[h].load_shared(ring_s + d * STAGE + h * 32 * LB);
                 uint4 wv[KB][2];
 #pragma unroll
                 for (int c = 0; c < KB; ++c)
 #pragma unroll
                     for (int b = 0; b < 2; ++b)
-                        wv[c][b] = *(const uint4*)(sp + c * W4_CHUNK_BYTES + b * 512 + lane * 16);
+                        wv[c][b] = lds128(ring_u + d * STAGE + c * W4_CHUNK_BYTES + b * 512);
                 float s[2][NT][4];
-                const uint8_t* xc = xs + (size_t)cc * KB * xchunk;
-                const float* xq = xsum + (size_t)cc * SG * 8 * NT + 2 * (lane & 3);
 #pragma unroll
                 for (int h = 0; h < 2 * KB; ++h) {  // 32 k each: two matrix steps
                     const W4Scale<FMT>& ws = w4s[G32 ? h : 0];
@@ -357,7 +366,7 @@ __global__ void __launch_bounds__(W4_THREADS, 1) linear_w4_kernel(const W4Args a
                     for (int t = 0; t < NT; ++t) {
 #pragma unroll
                         for (int p = 0; p < NP; ++p) {
-                            const uint4 xv = *(const uint4*)(xc + (h * NP + p) * xrow + xoff[t]);
+                            const uint4 xv = lds128(xc + xoff[t] + (h * NP + p) * XROW);
 #pragma unroll
                             for (int b = 0; b < 2; ++b) mma_16816(s[b][t], A[b][0], xv.x, xv.y);
 #pragma unroll
@@ -371,6 +380,8 @@ __global__ void __launch_bounds__(W4_THREADS, 1) linear_w4_kernel(const W4Args a
                                     acc[b][t][j] = fmaf(ws.scale(2 * b + (j >> 1)), s[b][t][j], acc[b][t][j]);
                     }
                 }
+                xc += XSTEP;
+                xq += SG * 8 * NT;
                 if (++cc == nc || i + 1 == len) {
                     // the run leaves the unit: its sum into the run's slot
                     const int first = run_of(cu * nc, n);
@@ -387,7 +398,10 @@ __global__ void __launch_bounds__(W4_THREADS, 1) linear_w4_kernel(const W4Args a
                             }
                     cc = 0;
                     ++cu;
+                    xc = xs_u;
+                    xq = xsum + 2 * (lane & 3);
                 }
+              }
             }
             // the next run's first steps are on their way while this one is wound up
             if (ph + 1 < phases) {
@@ -604,7 +618,7 @@ W4Plan w4_plan(const W4Layout& L, int format, int64_t tokens, bool x_f32, bool y
         const int kc = (steps + S - 1) / S;  // a CTA's share of K
         const int64_t cu = (L.units + P.C - 1) / P.C;
         // bytes of a step's x, and of its sums
-        const size_t xb = (size_t)KB * 2 * planes * tile * 64;
+        const size_t xb = (size_t)KB * 2 * planes * 8 * NT * 64;
         const size_t xq = P.offs ? (size_t)SG * 8 * NT * sizeof(float) : 0;
         // at most this much for x, the rest for the sums; phases of one length
         const int most_x = std::max(1, (int)((W4_SMEM - x_off - W4_WARPS * (slot + 8)) / (xb + xq)));

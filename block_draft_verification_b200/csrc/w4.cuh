@@ -118,18 +118,19 @@ template <int FMT>
 struct W4Scale {
     uint32_t raw[(FMT & DFLASH2_W4_SCALE_F32) ? 6 : (FMT & DFLASH2_W4_ZERO) ? 4 : 2];
     static constexpr int BYTES = w4_scale_bytes(FMT) / 8;
-    // p: the entries of this lane's four rows
-    __device__ __forceinline__ void load(const uint8_t* p) {
+    // a: shared address of the entries of this lane's four rows
+    __device__ __forceinline__ void load_shared(uint32_t a) {
         if constexpr ((FMT & DFLASH2_W4_SCALE_F32) != 0) {
-            const uint4 a = *(const uint4*)p;
-            const uint2 b = *(const uint2*)(p + 16);
-            raw[0] = a.x, raw[1] = a.y, raw[2] = a.z, raw[3] = a.w, raw[4] = b.x, raw[5] = b.y;
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(raw[0]), "=r"(raw[1]), "=r"(raw[2]), "=r"(raw[3])
+                         : "r"(a));
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(raw[4]), "=r"(raw[5]) : "r"(a + 16));
         } else if constexpr ((FMT & DFLASH2_W4_ZERO) != 0) {
-            const uint4 a = *(const uint4*)p;
-            raw[0] = a.x, raw[1] = a.y, raw[2] = a.z, raw[3] = a.w;
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(raw[0]), "=r"(raw[1]), "=r"(raw[2]), "=r"(raw[3])
+                         : "r"(a));
         } else {
-            const uint2 a = *(const uint2*)p;
-            raw[0] = a.x, raw[1] = a.y;
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(raw[0]), "=r"(raw[1]) : "r"(a));
         }
     }
     // i: 0 .. 3 for rows r, r + 8, r + 16, r + 24
