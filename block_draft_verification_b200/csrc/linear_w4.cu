@@ -653,8 +653,8 @@ W4Plan w4_plan(const W4Layout& L, int format, int64_t tokens, bool x_f32, bool y
         // for each filling of x (a chunk of a unit takes an SM about 25 ns)
         const int64_t batches = (cu + P.batch - 1) / P.batch;
         const int64_t fills = P.phases > 1 ? P.phases * batches : 1;
-        const int64_t cost = cu * kc * KB + batches * (S > 1 ? 40 : 20) +
-                             fills * (40 + (int64_t)P.phase * (int64_t)xb / 4096);
+        const int64_t cost = cu * kc * KB + batches * (S > 1 ? 30 + 10 * S : 20) +
+                             fills * (20 + (int64_t)P.phase * (int64_t)xb / 8192);
         if (best_cost < 0 || cost < best_cost) {
             best = P;
             best_cost = cost;
@@ -725,8 +725,10 @@ constexpr int64_t W4_MAX_TOKENS = 1 << 18;
 int run(const W4Call& c, cudaStream_t s) {
     W4Dev d;
     if (!device_info(d)) return DFLASH2_ECUDA;
-    if (!c.x_f32 && dfl_linear_w4_tc_ok(c)) return dfl_linear_w4_tc(c, d, s);
+    const bool tc = dfl_linear_w4_tc_ok(c);
+    if (tc && c.tokens > W4_FEW_TOKENS) return dfl_linear_w4_tc(c, d, s);
     const W4Plan P = w4_plan(c.L, c.format, c.tokens, c.x_f32, !c.y_bf16, d);
+    if (tc && c.tokens > 8 && P.phases > 2) return dfl_linear_w4_tc(c, d, s);
     W4Args a{};
     a.packed = (const uint8_t*)c.packed;
     a.N = c.L.N;

@@ -25,8 +25,12 @@ struct W4Dev {
     int clusters[9];
 };
 
-// Tokens from which the tensor-core kernel is the faster one.
-constexpr int64_t W4_TC_MIN_TOKENS = 16;
+// The tensor-core kernel takes more than this many tokens, and fewer (above 8) where
+// the other kernel would have to fill its shared memory with x more than twice over.
+// Other kernel and this one: 10,240 x 5,120, 13.6 and 23.2 us at 8 tokens, 20.9 and
+// 23.4 at 16, 51.5 and 23.7 at 17; 20,480 x 5,120 (x in two parts), 27.7 and 43.4 at
+// 9; 5,120 x 20,480 (x in four parts), 22.6 and 37.0 at 8, 83.5 and 37.1 at 9.
+constexpr int64_t W4_FEW_TOKENS = 16;
 
 bool dfl_linear_w4_tc_ok(const W4Call& c);
 int dfl_linear_w4_tc(const W4Call& c, const W4Dev& d, cudaStream_t s);

@@ -753,12 +753,11 @@ int launch_fmt(const CUtensorMap& map, const W4TcArgs& a, const W4Layout& L, int
 }  // namespace
 
 bool dfl_linear_w4_tc_ok(const W4Call& c) {
-    return c.x_vec && c.tokens > W4_TC_MIN_TOKENS && encode_fn() != nullptr;
+    return c.x_vec && !c.x_f32 && encode_fn() != nullptr;
 }
 
 int dfl_linear_w4_tc(const W4Call& c, const W4Dev& d, cudaStream_t s) {
     const W4Layout& L = c.L;
-    const int ntok = c.tokens <= 32 ? 32 : c.tokens <= 64 ? 64 : 128;
     W4TcArgs a{};
     a.packed = (const uint8_t*)c.packed;
     a.units = L.units;
@@ -766,31 +765,37 @@ int dfl_linear_w4_tc(const W4Call& c, const W4Dev& d, cudaStream_t s) {
     a.n_rows = L.N;
     a.ld = c.x_prev ? L.K : L.N;
     a.steps = L.steps;
-    a.tt = (int)((c.tokens + ntok - 1) / ntok);
-    a.tiles = (L.units + 3) / 4 * a.tt;
     a.y = c.y;
     a.y_bf16 = c.y_bf16;
     a.y_vec = L.N % 4 == 0 && (uintptr_t)c.y % 16 == 0;
     a.x = (const __nv_bfloat16*)c.x;
     a.x_prev = (const __nv_bfloat16*)c.x_prev;
     a.T = c.T;
-    // Cluster size: rounds of tiles times the length of one, in cycles: a step
-    // takes the longest of its MMAs (N / 2 cycles each), its weights' share of
-    // memory bandwidth (23 bytes a cycle and SM) and its instructions (codes, and
-    // N multiply-adds per summing warp and group); a tile's end about 2,000 more,
-    // and another 2,000 where sums cross CTAs.
-    const int64_t mma = (int64_t)L.kb * 4 * (ntok / 2), mem = 4 * L.step_bytes / 23;
-    const int64_t ins = (int64_t)L.kb * 140 + L.sg * (ntok + 60);
-    const int64_t step = std::max(mma, std::max(mem, ins));
+    // Tokens per tile and cluster size: rounds of tiles times the length of one, in
+    // cycles.  A chunk takes about 300 for its barriers and codes and, per group, 250,
+    // 370 or 690 for the sums of 32, 64 or 128 tokens (its MMAs and its weights'
+    // share of memory bandwidth are below that); a tile's end about 1,500 for each 64
+    // tokens, 4,800 where sums cross CTAs.  (10,240 x 5,120: 23.9, 24.9 and 32.8 us at
+    // 32, 64 and 128 tokens in groups of 128; 20,480 x 5,120 in groups of 64: 46, 50
+    // and 95 us.)
+    int ntok = 0;
     int64_t best = -1;
-    for (int S = 1; S <= 8 && S <= L.steps; S *= 2) {
-        const int C = (int)std::min<int64_t>(a.tiles, d.clusters[S]);
-        const int64_t cost = ((a.tiles + C - 1) / C) *
-                                 ((L.steps + S - 1) / S * step + 1000 + 8 * ntok + (S > 1 ? 2000 : 0));
-        if (best < 0 || cost < best) {
-            best = cost;
-            a.S = S;
-            a.C = C;
+    for (int n : {32, 64, 128}) {
+        const int tt = (int)((c.tokens + n - 1) / n);
+        const int64_t tiles = (L.units + 3) / 4 * tt;
+        const int64_t step = L.kb * 300 + L.sg * (n == 32 ? 250 : n == 64 ? 370 : 690);
+        for (int S = 1; S <= 8 && S <= L.steps; S *= 2) {
+            const int64_t C = std::min<int64_t>(tiles, d.clusters[S]);
+            const int64_t cost = ((tiles + C - 1) / C) * ((L.steps + S - 1) / S * step +
+                                                          (n == 128 ? 2 : 1) * (S > 1 ? 4800 : 1500));
+            if (best < 0 || cost < best) {
+                best = cost;
+                ntok = n;
+                a.S = S;
+                a.C = (int)C;
+                a.tt = tt;
+                a.tiles = tiles;
+            }
         }
     }
     CUtensorMap map;
