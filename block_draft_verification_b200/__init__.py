@@ -403,11 +403,7 @@ def _call(name, index, *args):
         raise DFlash2Error(name, rc)
 
 
-def _like(t, dtype, index):
-    if t.get_device() != index:
-        raise ValueError("dflash2 calls take tensors of one CUDA device")
-    if t.dtype != dtype:
-        raise TypeError("expected %s, got %s" % (dtype, t.dtype))
+_CODE = {torch.float32: F32, torch.bfloat16: BF16}
 
 
 class PackedW4:
@@ -459,14 +455,14 @@ def linear_w4(x, w4, out_dtype=None, out=None):
     if x.get_device() != index:
         raise ValueError("x and the weights are on one CUDA device")
     dx = _dtype(x)
-    x2, stride = _rows(x, K)
+    x2, stride = (x, K) if x.is_contiguous() else _rows(x, K)
     rows = x.numel() // K
     if rows > 16 and not x.is_contiguous() and (x2.data_ptr() | stride * x.element_size()) & 15:
         # rows that do not start on 16 bytes: the tensor cores' copies want them to
         x2, stride = x2.contiguous(), K
     oshape = shape[:-1] + (N,)
     if out is None:
-        out = torch.empty(oshape, dtype=out_dtype or x.dtype, device=x.device)
+        out = x.new_empty(oshape, dtype=out_dtype)
     elif out.shape != oshape or not out.is_contiguous() or out.get_device() != index or \
             (out_dtype is not None and out.dtype != out_dtype):
         raise ValueError("out is not a dense [..., N] tensor of the result's type")
@@ -523,23 +519,21 @@ def norm_residual(res, y, w_post=None, w_pre=None, gate=None, gate_act=GATE_LINE
         raise ValueError("dflash2 calls take tensors of one CUDA device")
     if res.shape != shape:
         raise ValueError("res and y have one shape")
-    dy, dr = _dtype(y), _dtype(res)
-    y2, ys = _rows(y, H)
-    r2, rs = _rows(res, H)
+    dy, dr = _CODE.get(dt), _CODE.get(res.dtype)
+    if dy is None or dr is None:
+        raise TypeError("expected float32 or bfloat16, got %s and %s" % (res.dtype, dt))
     rows = y.numel() // H if H else 0
-    wp = [None, None]
-    keep = []
-    for i, w in enumerate((w_post, w_pre)):
-        if w is not None:
-            _like(w, dt, index)
-            if w.dim() != 1 or w.shape[0] != H:
-                raise ValueError("norm weights are [H]")
-            if not w.is_contiguous():
-                keep.append(w := w.contiguous())
-            wp[i] = w.data_ptr()
-    gp, gs, rep = None, H, 1
+    for t in (w_post, w_pre, gate):
+        if t is not None:
+            if t.get_device() != index:
+                raise ValueError("dflash2 calls take tensors of one CUDA device")
+            if t.dtype is not dt:
+                raise TypeError("the gate and the weights have y's type")
+    for w in (w_post, w_pre):
+        if w is not None and (w.numel() != H or w.dim() != 1):
+            raise ValueError("norm weights are [H]")
+    gs, rep = H, 1
     if gate is not None:
-        _like(gate, dt, index)
         gshape = gate.shape
         if len(gshape) == 1 and gshape[0] == H:
             rep = max(rows, 1)
@@ -549,18 +543,28 @@ def norm_residual(res, y, w_post=None, w_pre=None, gate=None, gate_act=GATE_LINE
             rep = max(shape[1], 1)
         else:
             raise ValueError("gate is [H], [B, H] or like y")
-        g2, gs = (gate.contiguous(), H) if len(gshape) == 1 else _rows(gate, H)
-        gp = g2.data_ptr()
+        if not gate.is_contiguous():
+            gate, gs = (gate.contiguous(), H) if len(gshape) == 1 else _rows(gate, H)
+    y2, ys = (y, H) if y.is_contiguous() else _rows(y, H)
+    r2, rs = (res, H) if res.is_contiguous() else _rows(res, H)
+    if w_post is not None and not w_post.is_contiguous():
+        w_post = w_post.contiguous()
+    if w_pre is not None and not w_pre.is_contiguous():
+        w_pre = w_pre.contiguous()
+    h = None
     if out is None:
-        r_out = torch.empty_like(res, memory_format=torch.contiguous_format)
-        h = torch.empty_like(y, memory_format=torch.contiguous_format) if w_pre is not None else None
+        # (empty_like keeps a dense layout, which a transposed one is not)
+        r_out = torch.empty_like(res) if r2 is res else torch.empty(shape, dtype=res.dtype, device=y.device)
+        if w_pre is not None:
+            h = torch.empty_like(y) if y2 is y else torch.empty(shape, dtype=dt, device=y.device)
     else:
         r_out, h = out if w_pre is not None else (out, None)
         for t, like in ((r_out, res), (h, y)):
             if t is not None and (t.shape != shape or t.dtype != like.dtype or
                                   not t.is_contiguous() or t.get_device() != index):
                 raise ValueError("out is not a dense tensor like res (and y)")
-    _call("dflash2_norm_residual", index, r2.data_ptr(), dr, rs, y2.data_ptr(), dy, ys, gp, gs, rep,
-          gate_act, wp[0], wp[1], w_offset, scale, eps, rows, H, r_out.data_ptr(),
-          None if h is None else h.data_ptr())
+    _call("dflash2_norm_residual", index, r2.data_ptr(), dr, rs, y2.data_ptr(), dy, ys,
+          None if gate is None else gate.data_ptr(), gs, rep, gate_act,
+          None if w_post is None else w_post.data_ptr(), None if w_pre is None else w_pre.data_ptr(),
+          w_offset, scale, eps, rows, H, r_out.data_ptr(), None if h is None else h.data_ptr())
     return r_out if h is None else (r_out, h)

@@ -727,7 +727,19 @@ int run(const W4Call& c, cudaStream_t s) {
     if (!device_info(d)) return DFLASH2_ECUDA;
     const bool tc = dfl_linear_w4_tc_ok(c);
     if (tc && c.tokens > W4_FEW_TOKENS) return dfl_linear_w4_tc(c, d, s);
-    const W4Plan P = w4_plan(c.L, c.format, c.tokens, c.x_f32, !c.y_bf16, d);
+    // the plan of the thread's last shape is kept: a decode calls the same ones over
+    struct Last {
+        int64_t N, K, tokens;
+        int group, format, types, dev;
+        W4Plan P;
+    };
+    static thread_local Last last = {};
+    const int types = 2 * c.x_f32 + c.y_bf16;
+    if (last.N != c.L.N || last.K != c.L.K || last.tokens != c.tokens || last.group != c.L.group ||
+        last.format != c.format || last.types != types || last.dev != d.id)
+        last = {c.L.N, c.L.K, c.tokens, c.L.group, c.format, types, d.id,
+                w4_plan(c.L, c.format, c.tokens, c.x_f32, !c.y_bf16, d)};
+    const W4Plan& P = last.P;
     if (tc && c.tokens > 8 && P.phases > 2) return dfl_linear_w4_tc(c, d, s);
     W4Args a{};
     a.packed = (const uint8_t*)c.packed;
