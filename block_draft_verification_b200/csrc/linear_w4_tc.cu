@@ -4,7 +4,8 @@
 // A tile is 128 weight rows (four units) by up to 128 tokens.  Its K loop:
 //   warp 0       one bulk copy per packed step (64 or 128 k) of the tile into the W
 //                ring
-//   warp 2       TMA of the tokens' x (64 k boxes, 128-byte swizzle) into the X ring
+//   warp 2       TMA of the tokens' x (64 k boxes, 128-byte swizzle) into the chunk's
+//                stage
 //   warps 4-19   codes to exact bf16 integers q - zero, stored as the K-major,
 //                128-byte swizzled A tile of a 64 k chunk; a warp takes a unit, and
 //                each four warps every fourth chunk
@@ -41,9 +42,7 @@ constexpr int TW_ROWS = 128;            // weight rows per tile: four units
 constexpr int TW_DEQ = 16, TW_SUM = 8;  // warps
 constexpr int TW_THREADS = 32 * (4 + TW_DEQ + TW_SUM);
 constexpr int TW_SUB = TW_ROWS * 128;   // bytes of 64 k of A
-constexpr int TW_NA = 4;                // chunks in the A ring
-// Chunks in the X ring: it covers the latency of L2 and a chunk's MMAs.
-__host__ __device__ constexpr int tw_x_stages(int n) { return n == 128 ? 5 : 8; }
+constexpr int TW_NA = 4;                // chunks in the operand rings (A and x)
 // Registers: 896 threads are launched with 72 each, 64,512; 128 x 40 + 512 x 48 +
 // 256 x 136 use all of them after the split.
 
@@ -63,20 +62,23 @@ struct W4TcArgs {
 __host__ __device__ constexpr int tw_w_stage(int kb, int sg, int fmt) {
     return 4 * (kb * W4_CHUNK_BYTES + sg * w4_scale_bytes(fmt));
 }
-// Tokens whose sums are joined at a time at a tile's end.
-__host__ __device__ constexpr int tw_round(int n) { return n < 64 ? n : 64; }
-// Shared memory but for the W ring: 1 KB to align the start, the A and X rings,
-// a round's sums, the barriers.
-__host__ __device__ constexpr int tw_fixed(int n) {
-    return 1024 + TW_NA * TW_SUB + tw_x_stages(n) * n * 128 + tw_round(n) * TW_ROWS * 4 + 512;
+// Tokens whose sums are joined at a time at a tile's end: all of them, where shared
+// memory holds them beside a W ring long enough (not 128 with float scales or steps
+// of one chunk).
+__host__ __device__ constexpr int tw_round(int n, int kb, int fmt) {
+    return n == 128 && (kb == 1 || (fmt & DFLASH2_W4_SCALE_F32)) ? 64 : n;
+}
+// Shared memory but for the W ring: the operand rings, a round's sums, the barriers.
+__host__ __device__ constexpr int tw_fixed(int n, int kb, int fmt) {
+    return TW_NA * (TW_SUB + n * 128) + tw_round(n, kb, fmt) * TW_ROWS * 4 + 384;
 }
 // Steps in the W ring: what is left, and no more than 12.
 __host__ __device__ constexpr int tw_w_stages(int n, int kb, int sg, int fmt) {
-    const int w = (227 * 1024 - tw_fixed(n)) / tw_w_stage(kb, sg, fmt);
+    const int w = (227 * 1024 - tw_fixed(n, kb, fmt)) / tw_w_stage(kb, sg, fmt);
     return w < 12 ? w : 12;
 }
 __host__ __device__ constexpr int tw_smem(int n, int kb, int sg, int fmt) {
-    return tw_fixed(n) + tw_w_stages(n, kb, sg, fmt) * tw_w_stage(kb, sg, fmt);
+    return tw_fixed(n, kb, fmt) + tw_w_stages(n, kb, sg, fmt) * tw_w_stage(kb, sg, fmt);
 }
 constexpr int TW_AHEAD = 3;      // pairs of groups by which the scales are read before their sums
 constexpr int TW_PREFETCH = 12;  // steps between the request to L2 and the copy
@@ -207,12 +209,12 @@ struct TwEnd {
     int round;            // rounds before this tile's
 };
 
-// The sums of this CTA's K go to the CTAs of the cluster that write them, tw_round
+// The sums of this CTA's K go to the CTAs of the cluster that write them, NR
 // tokens at a time (half of them of either half of the columns), each CTA a share of
 // them; then they are added in rank order and written.
-template <int NTOK, int S>
+template <int NTOK, int NR, int S>
 __device__ __forceinline__ uint32_t tw_tile_end(const TwEnd& f, const uint64_t (&acc)[NTOK / 4]) {
-    constexpr int NC = NTOK / 2, NR = tw_round(NTOK), CPR = NR / 2, SHARE = NR / S;
+    constexpr int NC = NTOK / 2, CPR = NR / 2, SHARE = NR / S;
     const W4TcArgs& a = *f.a;
     uint32_t tries = f.tries;
     const int e = f.e, lane = e & 31;
@@ -340,22 +342,26 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
     constexpr int SG = G32 ? 2 : 1;
     constexpr int SB = w4_scale_bytes(FMT), LB = SB / 8;
     constexpr int STEP = KB * W4_CHUNK_BYTES + SG * SB;
-    constexpr int NA = TW_NA, NX = tw_x_stages(NTOK), NW = tw_w_stages(NTOK, KB, SG, FMT);
+    constexpr int NA = TW_NA, NW = tw_w_stages(NTOK, KB, SG, FMT);
     constexpr int WST = tw_w_stage(KB, SG, FMT);
     constexpr int XSUB = NTOK * 128;       // bytes of 64 k of x
     constexpr int NC = NTOK / 2;           // columns per summing warp
-    constexpr int NR = tw_round(NTOK);     // tokens per round of a tile's end
+    constexpr int NR = tw_round(NTOK, KB, FMT);  // tokens per round of a tile's end
     // TMEM holds two pairs of groups' accumulators; a pair is waited for, read and
     // given back at once (a wait that finds its barrier done still takes about 107
     // cycles, a good part of a group's products)
     constexpr int NB = 2;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* sa = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* sa = smem_raw;
+    if ((smem_u32(sa) & 1023u) != 0) {  // the swizzle's alignment, as declared
+        if (threadIdx.x == 0) atomicOr(&g_dev_err, (unsigned)ERR_PRODUCER);
+        return;
+    }
     uint8_t* sx = sa + NA * TW_SUB;
-    float* sp = (float*)(sx + NX * XSUB);  // [token][row] sums of a round
+    float* sp = (float*)(sx + NA * XSUB);  // [token][row] sums of a round
     uint8_t* sw = (uint8_t*)sp + NR * TW_ROWS * 4;
     uint64_t* bars = (uint64_t*)(sw + NW * WST);
-    uint32_t* s_tmem = (uint32_t*)(bars + 56);
+    uint32_t* s_tmem = (uint32_t*)(bars + 44);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = blockIdx.x % a.S, cl = blockIdx.x / a.S;
@@ -363,10 +369,10 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
     const int nst = (int)((int64_t)a.steps * (rank + 1) / a.S) - k0;
 
     const uint32_t wfull = smem_u32(bars), wempty = wfull + 8 * NW, full = wempty + 8 * NW,
-                   empty = full + 8 * NA, xfull = empty + 8 * NA, xempty = xfull + 8 * NX,
-                   tfull = xempty + 8 * NX, tempty = tfull + 8 * NB,
+                   empty = full + 8 * NA, tfull = empty + 8 * NA, tempty = tfull + 8 * NB,
                    mdone = tempty + 8 * NB, pready = mdone + 8, pfree = pready + 8;
-    static_assert(2 * NW + 2 * NA + 2 * NX + 2 * NB + 3 <= 56, "barriers");
+    // full: a chunk's A tile (an arrival per code warp) and its x (one, and the bytes)
+    static_assert(2 * NW + 2 * NA + 2 * NB + 3 <= 44, "barriers");
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NW; ++i) {
@@ -374,12 +380,8 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
             mbar_init(wempty + 8 * i, 4 * KB);
         }
         for (int i = 0; i < NA; ++i) {
-            mbar_init(full + 8 * i, 4);
+            mbar_init(full + 8 * i, 4 + 1);
             mbar_init(empty + 8 * i, 1);
-        }
-        for (int i = 0; i < NX; ++i) {
-            mbar_init(xfull + 8 * i, 1);
-            mbar_init(xempty + 8 * i, 1);
         }
         for (int i = 0; i < NB; ++i) {
             mbar_init(tfull + 8 * i, 1);
@@ -441,21 +443,21 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
             for (int64_t tile = cl; tile < a.tiles; tile += a.C) {
                 const int tok0 = (int)(tile % a.tt) * NTOK;
                 for (int s = 0; s < nst * KB; ++s, ++ci) {
-                    const int x = ci % NX;
-                    if (ci >= NX) tw_wait(xempty + 8 * x, (ci / NX - 1) & 1, tries);
-                    mbar_expect_tx(xfull + 8 * x, (uint32_t)XSUB);
+                    const int x = ci % NA;
+                    if (ci >= NA) tw_wait(empty + 8 * x, (ci / NA - 1) & 1, tries);
+                    mbar_expect_tx(full + 8 * x, (uint32_t)XSUB);
                     tw_load_x(smem_u32(sx + x * XSUB), &map_x, (k0 * KB + s) * W4_CHUNK, tok0,
-                              xfull + 8 * x);
+                              full + 8 * x);
                 }
             }
-            for (int q = ci > NX ? ci - NX : 0; q < ci; ++q) tw_wait(xfull + 8 * (q % NX), (q / NX) & 1, tries);
+            for (int q = ci > NA ? ci - NA : 0; q < ci; ++q) tw_wait(full + 8 * (q % NA), (q / NA) & 1, tries);
             tw_report(tries, ERR_PRODUCER);
         } else if (warp == 1) {
             // ---------------- MMA issuer: the whole warp waits, one lane issues
             const uint32_t elected = elect_lane();
-            int st = 0, sx_at = 0, pb = 0;
-            uint32_t par = 0, xpar = 0, tpar = 1;  // phases of the rings and (waited for) of TMEM
-            bool tried = false, xtried = false;
+            int st = 0, pb = 0;
+            uint32_t par = 0, tpar = 1;  // phases of the ring and (waited for) of TMEM
+            bool tried = false;
             for (int64_t tile = cl; tile < a.tiles; tile += a.C) {
                 const int64_t left = a.tokens - (tile % a.tt) * NTOK;
                 const uint32_t idesc =
@@ -470,21 +472,15 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
 #pragma unroll
                     for (int c = 0; c < KB; ++c) {
                         tw_wait(full + 8 * st, par, tries, tried);
-                        tw_wait(xfull + 8 * sx_at, xpar, tries, xtried);
                         tc_fence_after();
                         const uint64_t ao = smem_desc(smem_u32(sa + st * TW_SUB));
-                        const uint64_t xo = smem_desc(smem_u32(sx + sx_at * XSUB));
-                        const uint32_t done = empty + 8 * st, xdone = xempty + 8 * sx_at;
+                        const uint64_t xo = smem_desc(smem_u32(sx + st * XSUB));
+                        const uint32_t done = empty + 8 * st;
                         if (++st == NA) {
                             st = 0;
                             par ^= 1u;
                         }
-                        if (++sx_at == NX) {
-                            sx_at = 0;
-                            xpar ^= 1u;
-                        }
                         tried = mbar_test(full + 8 * st, par);
-                        xtried = mbar_test(xfull + 8 * sx_at, xpar);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
                             const bool first = SG == 2 ? kk % 2 == 0 : kk == 0 && c == 0;
@@ -492,7 +488,6 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
                                            idesc, first ? 0u : 1u);
                         }
                         mma_commit_elect(elected, done);
-                        mma_commit_elect(elected, xdone);
                     }
                     if (closes) {
                         mma_commit_elect(elected, tfull + 8 * pb);
@@ -658,13 +653,13 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
             // unrolled, their addresses constants.
             const TwEnd t{&a, sp, tries, rank, rt, tok0, ntok, e, half, q, pready, pfree, round};
             if (a.S == 1)
-                tries = tw_tile_end<NTOK, 1>(t, acc);
+                tries = tw_tile_end<NTOK, NR, 1>(t, acc);
             else if (a.S == 2)
-                tries = tw_tile_end<NTOK, 2>(t, acc);
+                tries = tw_tile_end<NTOK, NR, 2>(t, acc);
             else if (a.S == 4)
-                tries = tw_tile_end<NTOK, 4>(t, acc);
+                tries = tw_tile_end<NTOK, NR, 4>(t, acc);
             else
-                tries = tw_tile_end<NTOK, 8>(t, acc);
+                tries = tw_tile_end<NTOK, NR, 8>(t, acc);
             round += min(NTOK / NR, (ntok + NR / 2 - 1) / (NR / 2));
         }
         if (lane == 0) tw_report(tries, ERR_EPILOGUE);
@@ -774,8 +769,8 @@ int dfl_linear_w4_tc(const W4Call& c, const W4Dev& d, cudaStream_t s) {
     // Tokens per tile and cluster size: rounds of tiles times the length of one, in
     // cycles.  A chunk takes about 300 for its barriers and codes and, per group, 250,
     // 370 or 690 for the sums of 32, 64 or 128 tokens (its MMAs and its weights'
-    // share of memory bandwidth are below that); a tile's end about 1,500 for each 64
-    // tokens, 4,800 where sums cross CTAs.  (10,240 x 5,120: 23.9, 24.9 and 32.8 us at
+    // share of memory bandwidth are below that); each round of a tile's end about 1,500,
+    // 4,800 where sums cross CTAs.  (10,240 x 5,120: 23.9, 24.9 and 32.8 us at
     // 32, 64 and 128 tokens in groups of 128; 20,480 x 5,120 in groups of 64: 46, 50
     // and 95 us.)
     int ntok = 0;
@@ -783,11 +778,12 @@ int dfl_linear_w4_tc(const W4Call& c, const W4Dev& d, cudaStream_t s) {
     for (int n : {32, 64, 128}) {
         const int tt = (int)((c.tokens + n - 1) / n);
         const int64_t tiles = (L.units + 3) / 4 * tt;
+        const int ends = n / tw_round(n, L.kb, c.format);
         const int64_t step = L.kb * 300 + L.sg * (n == 32 ? 250 : n == 64 ? 370 : 690);
         for (int S = 1; S <= 8 && S <= L.steps; S *= 2) {
             const int64_t C = std::min<int64_t>(tiles, d.clusters[S]);
             const int64_t cost = ((tiles + C - 1) / C) * ((L.steps + S - 1) / S * step +
-                                                          (n == 128 ? 2 : 1) * (S > 1 ? 4800 : 1500));
+                                                          ends * (S > 1 ? 4800 : 1500));
             if (best < 0 || cost < best) {
                 best = cost;
                 ntok = n;
