@@ -17,6 +17,12 @@
 // the tensor core and the scale multiplies them in fp32.  The scaling costs 128 x
 // N fused multiply-adds a group beside 128 x N x group on the tensor core.
 //
+// Measured: 20,480 x 5,120 with 64 tokens (groups of 64) in 50 us, 5,120 x 20,480 with
+// 256 in 84 us (640 TFLOP/s), the conv of 32 x 8 tokens at H = 5,120 in 50 us.  With
+// codes, sums and tile ends left out the pipeline alone takes 30, 61 and 29 us: about
+// 480 cycles a chunk, the way from a free stage over the copy of x (about 1,100
+// cycles) to its MMAs in a ring of four; a tile's end costs 9 to 16 us of the rest.
+//
 // Tiles are taken by clusters of S CTAs that split K; the sums meet in
 // distributed shared memory in rank order: no workspace, no atomics.  S is the
 // one that leaves the SMs least idle.  Every wait is bounded (tw_wait); after one

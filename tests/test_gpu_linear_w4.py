@@ -81,6 +81,35 @@ def test_head_of_a_block(orc):
     check(orc, 4, 8, 151936, 5120, 128, rows=[0, 31, 32, 63, 75967, 75968, 151000, 151935])
 
 
+def test_offsets_past_32_bits(orc):
+    """Codes of more than 2^31 bytes, and outputs of more than 2^31 elements."""
+    need_cuda()
+    N, K, group = 300000, 16384, 128
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(21)
+    q = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device="cuda", generator=gen)
+    s = (torch.rand((N, K // group), device="cuda", generator=gen) * 0.01).bfloat16()
+    w = dfl.PackedW4(q, s)
+    rows = np.array([0, 131071, 262144, 262145, N - 33, N - 1])
+    qh, sh = to_host(q[rows]), to_host(s[rows])
+    del q, s
+    rng = np.random.default_rng(22)
+    x = activations(rng, (20, K), "bf16")
+    ref, mag = orc.linear_w4(x, qh, sh)
+    for tokens in (3, 20):
+        y = dfl.linear_w4(to_dev(x[:tokens]), w, out_dtype=torch.float32)
+        assert_within(f64(y[:, rows.tolist()]), ref[:tokens], mag[:tokens], K, 1, False, "packed")
+    del w, y
+    tokens, N, K = 2 ** 18, 8300, 32
+    q, s, _ = weights(rng, N, K, 32)
+    x = torch.randn((tokens, K), device="cuda", generator=gen).bfloat16()
+    y = dfl.linear_w4(x, packed(q, s, None))
+    at = [0, 2 ** 17, tokens - 2, tokens - 1]
+    ref, mag = orc.linear_w4(to_host(x[at]), q, s)
+    assert_within(f64(y[at]), ref, mag, K, 1, True, "output")
+    assert dfl.device_errors() == 0
+
+
 def test_exact_small_integers(orc):
     """Integer activations and power-of-two scales: every sum is exact, so every bit is."""
     need_cuda()

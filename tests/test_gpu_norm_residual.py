@@ -175,6 +175,22 @@ def test_rows_do_not_depend_on_the_batch_and_nothing_else_is_written():
     assert dfl.norm_residual(e, e, w_pre=torch.ones(64, device="cuda"))[1].shape == (0, 64)
 
 
+def test_offsets_past_32_bits(orc):
+    """More than 2^31 elements, vectors and single elements."""
+    need_cuda()
+    for H in (4096, 4097):
+        rows = 530000
+        y = torch.empty((rows, H), dtype=torch.bfloat16, device="cuda").normal_()
+        res = y.clone()
+        w = torch.full((H,), 1.25, dtype=torch.bfloat16, device="cuda")
+        r, h = dfl.norm_residual(res, y, w, w, out=(res, torch.empty_like(y)))
+        at = [0, 524287, 524288, rows - 1]
+        d = dict(res=to_host(y[at]), y=to_host(y[at]), gate=None, w_post=to_host(w), w_pre=to_host(w))
+        want = orc.norm_residual(d["res"], d["y"], d["w_post"], d["w_pre"], eps=float(np.float32(1e-6)))
+        compare((r[at], h[at]), want, d, H, 1e-6)
+        del y, res, r, h
+
+
 def test_binding_refusals():
     need_cuda()
     y = torch.zeros((2, 3, 16), dtype=torch.bfloat16, device="cuda")
