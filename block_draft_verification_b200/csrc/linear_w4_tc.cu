@@ -194,7 +194,7 @@ __device__ __forceinline__ void mma_commit_elect(uint32_t elected, uint32_t bar)
         "r"(elected)
         : "memory");
 }
-// 32 lanes x N consecutive fp32 columns, no wait.
+// 32 lanes x 16 consecutive fp32 columns, no wait.
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(TW_THREADS, 1)
             const int rt = (int)(tile / a.tt);
             const int tok0 = (int)(tile - (int64_t)rt * a.tt) * NTOK;
             const int ntok = (int)min((int64_t)NTOK, a.tokens - tok0);
-            // this row's scales, TW_AHEAD steps ahead of their use, straight from the
+            // this row's scales, TW_AHEAD pairs ahead of their use, straight from the
             // packed steps (in L2 by then)
             const uint8_t* sp0 = a.packed + w4_block((int64_t)rt * 4 + q, a.steps, k0, STEP) + KB * W4_CHUNK_BYTES +
                                  (lane & 7) * LB + (lane >> 3) * ((FMT & DFLASH2_W4_SCALE_F32) ? 4 : 2);
