@@ -776,7 +776,7 @@ int dfl_linear_w4_tc(const W4Call& c, const W4Dev& d, cudaStream_t s) {
     // cycles.  A chunk takes about 300 for its barriers and codes and, per group, 250,
     // 370 or 690 for the sums of 32, 64 or 128 tokens (its MMAs and its weights'
     // share of memory bandwidth are below that); each round of a tile's end about 1,500,
-    // 4,800 where sums cross CTAs.  (10,240 x 5,120: 23.9, 24.9 and 32.8 us at
+    // 6,500 where sums cross CTAs.  (10,240 x 5,120: 23.9, 24.9 and 32.8 us at
     // 32, 64 and 128 tokens in groups of 128; 20,480 x 5,120 in groups of 64: 46, 50
     // and 95 us.)
     int ntok = 0;
@@ -789,7 +789,7 @@ int dfl_linear_w4_tc(const W4Call& c, const W4Dev& d, cudaStream_t s) {
         for (int S = 1; S <= 8 && S <= L.steps; S *= 2) {
             const int64_t C = std::min<int64_t>(tiles, d.clusters[S]);
             const int64_t cost = ((tiles + C - 1) / C) * ((L.steps + S - 1) / S * step +
-                                                          ends * (S > 1 ? 4800 : 1500));
+                                                          ends * (S > 1 ? 6500 : 1500));
             if (best < 0 || cost < best) {
                 best = cost;
                 ntok = n;

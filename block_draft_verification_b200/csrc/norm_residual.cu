@@ -10,9 +10,8 @@
 // by one CTA sized to it; rows too long for its registers are read again from
 // cache (three passes).
 //
-// Measured: 4,096 rows of 5,120 with an fp32 residual and a gate per token in 63.5 us,
-// 4.6 TB/s (72 % of the copy rate; two vectors a thread, 320 threads: one vector and
-// 640 threads take 110 us, four and 160 take 64); 256 rows in 5.3 us and 8 rows in
+// Measured: 4,096 rows of 5,120 with an fp32 residual and a gate per token in 54.1 us,
+// 5.4 TB/s (84 % of the copy rate; two vectors a thread, 320 threads); 256 rows in 5.3 us and 8 rows in
 // 3.9 us, which is the two barriers and a launch.
 #include <algorithm>
 
@@ -118,8 +117,13 @@ __device__ __forceinline__ float block_sum(float v, float* buf) {
 // elements of the row (blockDim V W >= H; W = 8 wants H a multiple of 8 and
 // 16-byte rows, W = 1 takes any).  Everything a row needs from memory is
 // requested before its first sum.
+// Two packs of 16-bit elements fit 64 registers (the compiler takes 94 of its own
+// accord), and with them three rows of 5,120 are in flight on an SM instead of two:
+// 63.6 -> 54.1 us; fp32 packs would spill, and one element at a time is slower when
+// it is told anything (7.2 -> 9.6 us at 1,001 x 1,023).
 template <typename XT, typename RT, int W, int V>
-__global__ void __launch_bounds__(512) norm_residual_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(512, W == 8 && V == 2 && sizeof(XT) == 2 ? 2 : 0)
+    norm_residual_kernel(const NormArgs a) {
     __shared__ float buf[2][32];
     const int np = (int)(a.H / W);
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
