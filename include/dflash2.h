@@ -476,9 +476,11 @@ DFLASH2_API int dflash2_w4_pack(const uint8_t* q, const void* scale, const uint8
  * The codes minus their zero points are multiplied exactly (fp32 activations
  * as three bf16 parts that add up to the value), sums are fp32, with one
  * rounding at a bf16 output; |x| below 2^-100 may lose its last bits.  A
- * given shape on a given device always rounds the same way; a token's last
- * bits may depend on how many tokens the call has.  No workspace: calls may
- * run at the same time on any streams.
+ * NaN or an infinity in x leaves its token without a finite output (NaN, where
+ * infinities may meet with either sign) and touches no other token.  A given
+ * shape on a given device always rounds the same way; a token's last bits may
+ * depend on how many tokens the call has.  No workspace: calls may run at the
+ * same time on any streams.
  */
 DFLASH2_API int dflash2_linear_w4(const void* x, int dtype, int64_t x_stride, int64_t tokens,
                                   const void* packed, int64_t N, int64_t K, int group, int format,
