@@ -62,7 +62,7 @@ struct W4Args {
     int phase, phases;   // steps of x in shared memory at a time, and how often
     int batch;           // units whose sums are in shared memory at a time
     int slots;           // partial sums per unit
-    int x_off, xsum_off, part_off, counts_off;  // byte offsets in shared memory
+    int x_off, part_off, counts_off;  // byte offsets in shared memory
 };
 
 // Shared memory of a step in a warp's ring: the lanes' 16-byte pieces of its
@@ -164,9 +164,8 @@ __device__ __forceinline__ void load_x8(const XT* row, int64_t k, int64_t K, boo
 
 // XT: activation type; NT: 8-token tiles; FMT: scale format; G32: groups of
 // 32 (two per chunk); KB: chunks per step (2 where the group is a multiple of
-// 128: one scaling, one set of loads and one turn of the loop for 128 k);
-// OFFS: codes to operands by offset (w4.cuh).
-template <typename XT, int NT, int FMT, bool G32, int KB, bool OFFS>
+// 128: one scaling, one set of loads and one turn of the loop for 128 k).
+template <typename XT, int NT, int FMT, bool G32, int KB>
 __global__ void __launch_bounds__(W4_THREADS, 1) linear_w4_kernel(const W4Args a) {
     static_assert(!(G32 && KB > 1), "groups of 32 end inside a chunk");
     constexpr int NP = sizeof(XT) == 4 ? 3 : 1;
@@ -185,14 +184,12 @@ __global__ void __launch_bounds__(W4_THREADS, 1) linear_w4_kernel(const W4Args a
     const int64_t u0 = a.units * cl / a.C, u1 = a.units * (cl + 1) / a.C;
 
     // shared memory: the warps' rings, x [chunk][half][plane][8 NT tokens][32 k]
-    // bf16 (64-byte rows), the sums of x [step][group of the step][8 NT tokens]
-    // (OFFS), then the partial sums [unit of the batch][slot][NT * 8][32 lanes]
-    // fp32 and the units' slot counts
+    // bf16 (64-byte rows), then the partial sums [unit of the batch][slot][NT * 8]
+    // [32 lanes] fp32 and the units' slot counts
     constexpr int XROW = NT * 8 * 64, XSTEP = KB * 2 * NP * XROW;
     const uint32_t ring = smem_u32(smem + warp * (D * STAGE));
     const uint32_t ring_u = ring + lane * 16, ring_s = ring + KB * W4_CHUNK_BYTES + lane * LB;
     uint8_t* xs = smem + a.x_off;
-    float* xsum = (float*)(smem + a.xsum_off);
     float* part = (float*)(smem + a.part_off);
     constexpr int PU = NT * 8 * 32;  // floats of one slot
 
@@ -277,33 +274,6 @@ __global__ void __launch_bounds__(W4_THREADS, 1) linear_w4_kernel(const W4Args a
                     for (int i = threadIdx.x; i < nu * a.slots * PU; i += W4_THREADS) part[i] = 0.0f;
                 __syncthreads();
             }
-            if constexpr (OFFS) {
-                // sums of x over each group's part of a step: four lanes per token
-                if (new_x) {
-                    constexpr int HALVES = 2 * KB / SG;  // 32-k rows per sum
-                    const int items = nc * SG * 8 * NT * 4;
-                    for (int i = threadIdx.x; i < items; i += W4_THREADS) {
-                        const int c8 = i & 3, r = i >> 2, t = r % (8 * NT), pc = r / (8 * NT);
-                        float v = 0.0f;
-                        if (t < nt) {
-#pragma unroll
-                            for (int h = 0; h < HALVES; ++h) {
-                                const uint4 q = *(const uint4*)(xs + (size_t)(pc * HALVES + h) * XROW +
-                                                                t * 64 + c8 * 16);
-                                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    v += __uint_as_float(w[e] << 16) + __uint_as_float(w[e] & 0xFFFF0000u);
-                            }
-                        }
-                        v += __shfl_xor_sync(FULL, v, 1);  // items is a multiple of 32: whole warps
-                        v += __shfl_xor_sync(FULL, v, 2);
-                        if (c8 == 0) xsum[r] = v;
-                    }
-                    __syncthreads();
-                }
-            }
-
             // a lane's rows of x: tokens past the tile's last read that one's, and
             // their columns of the products are never looked at
             uint32_t xoff[NT];
@@ -318,7 +288,6 @@ __global__ void __launch_bounds__(W4_THREADS, 1) linear_w4_kernel(const W4Args a
                     for (int j = 0; j < 4; ++j) acc[b][t][j] = 0.0f;
             const uint32_t xs_u = smem_u32(xs);
             uint32_t xc = xs_u + cc * XSTEP;
-            const float* xq = xsum + (size_t)cc * SG * 8 * NT + 2 * (lane & 3);
             for (int i0 = 0; i0 < len; i0 += D) {
 #pragma unroll
               for (int d = 0; d < D; ++d) {  // the ring's stages in turn
@@ -340,18 +309,12 @@ __global__ void __launch_bounds__(W4_THREADS, 1) linear_w4_kernel(const W4Args a
                 for (int h = 0; h < 2 * KB; ++h) {  // 32 k each: two matrix steps
                     const W4Scale<FMT>& ws = w4s[G32 ? h : 0];
                     if (h == 0 || G32) {
-                        // the sums start (at zero, or at minus the offset's share)
 #pragma unroll
-                        for (int t = 0; t < NT; ++t) {
-                            float2 q = make_float2(0.0f, 0.0f);
-                            if constexpr (OFFS) q = *(const float2*)(xq + (G32 ? h : 0) * 8 * NT + 8 * t);
+                        for (int b = 0; b < 2; ++b)
 #pragma unroll
-                            for (int b = 0; b < 2; ++b)
+                            for (int t = 0; t < NT; ++t)
 #pragma unroll
-                                for (int j = 0; j < 4; ++j)
-                                    s[b][t][j] =
-                                        OFFS ? -ws.zero16(2 * b + (j >> 1)) * ((j & 1) ? q.y : q.x) : 0.0f;
-                        }
+                                for (int j = 0; j < 4; ++j) s[b][t][j] = 0.0f;
                     }
                     uint32_t A[2][2][4];  // [16-row half][matrix step]
 #pragma unroll
@@ -362,13 +325,8 @@ __global__ void __launch_bounds__(W4_THREADS, 1) linear_w4_kernel(const W4Args a
                         for (int q = 0; q < 2; ++q)
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                if constexpr (OFFS) {
-                                    A[b][q][2 * e] = w4_pair_offset(wl, 2 * q + e);
-                                    A[b][q][2 * e + 1] = w4_pair_offset(wh, 2 * q + e);
-                                } else {
-                                    A[b][q][2 * e] = w4_pair_exact(wl, 2 * q + e, ws.zero2(2 * b));
-                                    A[b][q][2 * e + 1] = w4_pair_exact(wh, 2 * q + e, ws.zero2(2 * b + 1));
-                                }
+                                A[b][q][2 * e] = w4_pair_exact(wl, 2 * q + e, ws.zero2(2 * b));
+                                A[b][q][2 * e + 1] = w4_pair_exact(wh, 2 * q + e, ws.zero2(2 * b + 1));
                             }
                     }
 #pragma unroll
@@ -390,7 +348,6 @@ __global__ void __launch_bounds__(W4_THREADS, 1) linear_w4_kernel(const W4Args a
                     }
                 }
                 xc += XSTEP;
-                xq += SG * 8 * NT;
                 if (++cc == nc || i + 1 == len) {
                     // the run leaves the unit: its sum into the run's slot
                     const int first = run_of(cu * nc, n);
@@ -408,7 +365,6 @@ __global__ void __launch_bounds__(W4_THREADS, 1) linear_w4_kernel(const W4Args a
                     cc = 0;
                     ++cu;
                     xc = xs_u;
-                    xq = xsum + 2 * (lane & 3);
                 }
               }
             }
@@ -575,7 +531,7 @@ bool device_info(W4Dev& d) {
         d = known[d.id];
         return true;
     }
-    auto* k = linear_w4_kernel<__nv_bfloat16, 1, 0, false, 1, true>;
+    auto* k = linear_w4_kernel<__nv_bfloat16, 1, 0, false, 1>;
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, W4_SMEM) != cudaSuccess)
         return false;
     for (int S = 1; S <= 8; S *= 2) {
@@ -600,11 +556,10 @@ bool device_info(W4Dev& d) {
 
 // Cluster size, clusters, and the shared-memory split of one call.
 struct W4Plan {
-    int S, C, tile, NT, KB, SG, steps, phase, phases, batch, slots, x_off, xsum_off, part_off, counts_off;
-    bool offs;
+    int S, C, tile, NT, KB, SG, steps, phase, phases, batch, slots, x_off, part_off, counts_off;
     size_t smem;
 };
-W4Plan w4_plan(const W4Layout& L, int format, int64_t tokens, bool x_f32, bool y_f32, const W4Dev& d) {
+W4Plan w4_plan(const W4Layout& L, int format, int64_t tokens, bool x_f32, const W4Dev& d) {
     W4Plan best{};
     int64_t best_cost = -1;
     const int planes = x_f32 ? 3 : 1;
@@ -622,20 +577,16 @@ W4Plan w4_plan(const W4Layout& L, int format, int64_t tokens, bool x_f32, bool y
         P.KB = KB;
         P.SG = SG;
         P.steps = steps;
-        P.offs = !x_f32 && !y_f32;
         P.C = (int)std::min<int64_t>(L.units, d.clusters[S]);
         const int kc = (steps + S - 1) / S;  // a CTA's share of K
         const int64_t cu = (L.units + P.C - 1) / P.C;
-        // bytes of a step's x, and of its sums
-        const size_t xb = (size_t)KB * 2 * planes * 8 * NT * 64;
-        const size_t xq = P.offs ? (size_t)SG * 8 * NT * sizeof(float) : 0;
+        const size_t xb = (size_t)KB * 2 * planes * 8 * NT * 64;  // bytes of a step's x
         // at most this much for x, the rest for the sums; phases of one length
-        const int most_x = std::max(1, (int)((W4_SMEM - x_off - W4_WARPS * (slot + 8)) / (xb + xq)));
+        const int most_x = std::max(1, (int)((W4_SMEM - x_off - W4_WARPS * (slot + 8)) / xb));
         P.phases = (kc + most_x - 1) / most_x;
         P.phase = (kc + P.phases - 1) / P.phases;
         P.x_off = x_off;
-        P.xsum_off = x_off + (int)(P.phase * xb);
-        P.part_off = x_off + (int)(P.phase * (xb + xq));
+        P.part_off = x_off + (int)(P.phase * xb);
         const size_t left = W4_SMEM - P.part_off;
         // a unit's items are in ceil((nc - 1) / shortest run) + 1 runs at most
         for (P.batch = (int)std::min<int64_t>(cu, left / slot); P.batch >= 1; --P.batch) {
@@ -672,9 +623,9 @@ W4Plan w4_plan(const W4Layout& L, int format, int64_t tokens, bool x_f32, bool y
     return best;
 }
 
-template <typename XT, int NT, int FMT, bool G32, int KB, bool OFFS>
+template <typename XT, int NT, int FMT, bool G32, int KB>
 int launch(const W4Args& a, const W4Plan& P, int dev, cudaStream_t s) {
-    auto* k = linear_w4_kernel<XT, NT, FMT, G32, KB, OFFS>;
+    auto* k = linear_w4_kernel<XT, NT, FMT, G32, KB>;
     {
         static std::mutex mu;
         static bool attr_set[64] = {};
@@ -701,30 +652,28 @@ int launch(const W4Args& a, const W4Plan& P, int dev, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, k, a) == cudaSuccess ? DFLASH2_OK
                                                          : (cudaGetLastError(), DFLASH2_ECUDA);
 }
-template <typename XT, int FMT, bool G32, int KB, bool OFFS>
+template <typename XT, int FMT, bool G32, int KB>
 int launch_nt(const W4Args& a, const W4Plan& P, int dev, cudaStream_t s) {
     switch (P.NT) {
-        case 1: return launch<XT, 1, FMT, G32, KB, OFFS>(a, P, dev, s);
-        case 2: return launch<XT, 2, FMT, G32, KB, OFFS>(a, P, dev, s);
-        default: return launch<XT, 4, FMT, G32, KB, OFFS>(a, P, dev, s);
+        case 1: return launch<XT, 1, FMT, G32, KB>(a, P, dev, s);
+        case 2: return launch<XT, 2, FMT, G32, KB>(a, P, dev, s);
+        default: return launch<XT, 4, FMT, G32, KB>(a, P, dev, s);
     }
 }
-template <typename XT, int FMT, bool OFFS>
+template <typename XT, int FMT>
 int launch_group(const W4Args& a, const W4Plan& P, int dev, cudaStream_t s) {
-    if (P.KB == 2) return launch_nt<XT, FMT, false, 2, OFFS>(a, P, dev, s);
-    return P.SG == 2 ? launch_nt<XT, FMT, true, 1, OFFS>(a, P, dev, s)
-                         : launch_nt<XT, FMT, false, 1, OFFS>(a, P, dev, s);
+    if (P.KB == 2) return launch_nt<XT, FMT, false, 2>(a, P, dev, s);
+    return P.SG == 2 ? launch_nt<XT, FMT, true, 1>(a, P, dev, s)
+                         : launch_nt<XT, FMT, false, 1>(a, P, dev, s);
 }
-template <typename XT, bool OFFS>
+template <typename XT>
 int launch_fmt(const W4Args& a, const W4Plan& P, int format, int dev, cudaStream_t s) {
-    if (format & DFLASH2_W4_SCALE_F32) return launch_group<XT, 2, OFFS>(a, P, dev, s);
-    if (format & DFLASH2_W4_ZERO) return launch_group<XT, 1, OFFS>(a, P, dev, s);
-    return launch_group<XT, 0, OFFS>(a, P, dev, s);
+    if (format & DFLASH2_W4_SCALE_F32) return launch_group<XT, 2>(a, P, dev, s);
+    if (format & DFLASH2_W4_ZERO) return launch_group<XT, 1>(a, P, dev, s);
+    return launch_group<XT, 0>(a, P, dev, s);
 }
 int launch_any(const W4Args& a, const W4Plan& P, int format, bool x_f32, int dev, cudaStream_t s) {
-    if (x_f32) return launch_fmt<float, false>(a, P, format, dev, s);
-    return P.offs ? launch_fmt<__nv_bfloat16, true>(a, P, format, dev, s)
-                  : launch_fmt<__nv_bfloat16, false>(a, P, format, dev, s);
+    return x_f32 ? launch_fmt<float>(a, P, format, dev, s) : launch_fmt<__nv_bfloat16>(a, P, format, dev, s);
 }
 
 constexpr int W4_FORMATS = DFLASH2_W4_ZERO | DFLASH2_W4_SCALE_F32 | DFLASH2_W4_TAPS;
@@ -739,15 +688,14 @@ int run(const W4Call& c, cudaStream_t s) {
     // the plan of the thread's last shape is kept: a decode calls the same ones over
     struct Last {
         int64_t N, K, tokens;
-        int group, format, types, dev;
+        int group, format, x_f32, dev;
         W4Plan P;
     };
     static thread_local Last last = {};
-    const int types = 2 * c.x_f32 + c.y_bf16;
     if (last.N != c.L.N || last.K != c.L.K || last.tokens != c.tokens || last.group != c.L.group ||
-        last.format != c.format || last.types != types || last.dev != d.id)
-        last = {c.L.N, c.L.K, c.tokens, c.L.group, c.format, types, d.id,
-                w4_plan(c.L, c.format, c.tokens, c.x_f32, !c.y_bf16, d)};
+        last.format != c.format || last.x_f32 != c.x_f32 || last.dev != d.id)
+        last = {c.L.N, c.L.K, c.tokens, c.L.group, c.format, c.x_f32, d.id,
+                w4_plan(c.L, c.format, c.tokens, c.x_f32, d)};
     const W4Plan& P = last.P;
     if (tc && c.tokens > 8 && P.phases > 2) return dfl_linear_w4_tc(c, d, s);
     W4Args a{};
@@ -772,7 +720,6 @@ int run(const W4Call& c, cudaStream_t s) {
     a.batch = P.batch;
     a.slots = P.slots;
     a.x_off = P.x_off;
-    a.xsum_off = P.xsum_off;
     a.part_off = P.part_off;
     a.counts_off = P.counts_off;
     return launch_any(a, P, c.format, c.x_f32, d.id, s);

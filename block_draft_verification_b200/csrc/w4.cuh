@@ -31,15 +31,13 @@
 // Rows past N have scale 0; the K tail of a last half chunk has codes equal
 // to its zero point and, where it is a group of its own, scale 0.
 //
-// Codes to operands: 0x4180 | q << 3 is the bf16 value 16 + q.
-//   - exact: subtracting (16 + zero) leaves q - zero, an integer below 16 in
-//     magnitude, exactly.  The products with x then accumulate in fp32 with no
-//     rounding of the weights, and the group's scale multiplies the fp32 sum.
-//   - offset: no subtraction; the sum starts at -(16 + zero) * sum of x instead of
-//     zero.  A third fewer instructions, but the fp32 sum passes through
-//     magnitudes a few times those of the result, and its last bits go with them
-//     (about 2e-6 of the result): it serves bf16 outputs, whose own rounding is a
-//     thousand times that.
+// Codes to operands: 0x4180 | q << 3 is the bf16 value 16 + q; subtracting
+// (16 + zero) leaves q - zero, an integer below 16 in magnitude, exactly.  The
+// products with x then accumulate in fp32 with no rounding of the weights, and the
+// group's scale multiplies the fp32 sum.  (Leaving 16 + zero in and starting the sum
+// at -(16 + zero) times the sum of x saves the subtraction, but the sum then passes
+// through 16 to 31 times |x| of every channel, and a channel far above the rest
+// takes the others' last bits even where its own code is the zero point: not done.)
 #pragma once
 
 #include "common.cuh"
@@ -100,13 +98,10 @@ __device__ __forceinline__ uint32_t w4_and_or(uint32_t w, uint32_t mask, uint32_
     asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(t) : "r"(w), "r"(mask), "r"(magic));
     return t;
 }
-// The pair (2 j, 2 j + 1) of a word as bf16x2, plus 16 (zero points left in) ...
-__device__ __forceinline__ uint32_t w4_pair_offset(uint32_t w, int j) {
-    return w4_and_or(w4_turn(w, 4 * j), 0x00780078u, 0x41804180u);
-}
-// ... and minus the zero points; zz = bf16x2 of (16 + zero) twice.
+// The pair (2 j, 2 j + 1) of a word as bf16x2, minus the zero points; zz = bf16x2
+// of (16 + zero) twice.
 __device__ __forceinline__ uint32_t w4_pair_exact(uint32_t w, int j, uint32_t zz) {
-    const uint32_t t = w4_pair_offset(w, j);
+    const uint32_t t = w4_and_or(w4_turn(w, 4 * j), 0x00780078u, 0x41804180u);
     __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&t),
                                *reinterpret_cast<const __nv_bfloat162*>(&zz));
     return *reinterpret_cast<uint32_t*>(&d);
@@ -142,12 +137,6 @@ struct W4Scale {
         if constexpr (FMT == 0) return 0x41C041C0u;  // 16 + 8
         const uint32_t w = raw[((FMT & DFLASH2_W4_SCALE_F32) ? 4 : 2) + (i >> 1)];
         return (i & 1) ? __byte_perm(w, 0, 0x3232) : __byte_perm(w, 0, 0x1010);
-    }
-    // 16 + zero
-    __device__ __forceinline__ float zero16(int i) const {
-        if constexpr (FMT == 0) return 24.0f;
-        const uint32_t w = raw[((FMT & DFLASH2_W4_SCALE_F32) ? 4 : 2) + (i >> 1)];
-        return __uint_as_float((i & 1) ? (w & 0xFFFF0000u) : (w << 16));
     }
 };
 

@@ -328,3 +328,45 @@ def test_a_pass_of_head_and_step(orc):
     top = np.sort(ref, 1)[:, -2:]
     clear = (top[:, 1] - top[:, 0]) > 2 * sum_bound(H, 1) * mag.max(1)
     np.testing.assert_array_equal(to_host(tok).reshape(-1)[clear], ref.argmax(1)[clear])
+
+
+def silence(q, z, group, ks):
+    """Sets every row's code at the columns ks to its zero point: their products are zero."""
+    q = q.copy()
+    for k in ks:
+        c = np.full(len(q), 8, np.uint8) if z is None else z[:, k // group]
+        q[:, k // 2] = (q[:, k // 2] & 0x0F) | (c << 4) if k & 1 else (q[:, k // 2] & 0xF0) | c
+    return q
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("zeros,f32_scale", [(False, False), (True, False), (True, True)])
+@pytest.mark.parametrize("large", [1e3, 1e6, 1e9])
+def test_large_activations_on_zero_points_leave_no_trace(orc, group, zeros, f32_scale, large):
+    """Channels far above the rest whose codes are the zero point: their products are exactly
+    zero, so the others keep the bound of a sum without them, whatever the output's type."""
+    need_cuda()
+    rng = np.random.default_rng(group + int(np.log10(large)))
+    N, K = 70, 1024
+    q, s, z = weights(rng, N, K, group, zeros, f32_scale)
+    ks = [0, 5, 130, 131, 600, 1023]
+    q = silence(q, z, group, ks)
+    w = packed(q, s, z)
+    for tokens in (1, 3, 8, 11, 16, 20, 70):
+        x = activations(rng, (tokens, K), "f32") + np.float32(0.5)
+        x[:, ks] *= np.float32(large)
+        x = synth.to_bf16_bits(x)
+        ref, mag = orc.linear_w4(x, q, s, z)
+        for out in (torch.bfloat16, torch.float32):
+            y = dfl.linear_w4(to_dev(x), w, out_dtype=out)
+            assert_within(f64(y), ref, mag, K, 1, out == torch.bfloat16, "%d tokens" % tokens)
+    B, T = 2, 4
+    q, s, z = weights(rng, 2 * K, K, group, zeros, f32_scale)
+    q = silence(q, z, group, ks)
+    x, xp = activations(rng, (B, T, K), "f32"), activations(rng, (B, K), "f32")
+    x[:, :, ks] *= np.float32(large)
+    x, xp = synth.to_bf16_bits(x), synth.to_bf16_bits(xp)
+    out = dfl.dynconv2(to_dev(x), to_dev(xp), packed(q, s, z, taps=True))
+    ref, mag = orc.dynconv2_w4(x, xp, q, s, z)
+    assert_within(f64(out), ref, mag, K, 1, True, "conv", factor=1.0 + 2 / 34)
+    assert dfl.device_errors() == 0
