@@ -10,11 +10,9 @@
 // by one CTA sized to it; rows too long for its registers are read again from
 // cache (three passes).
 //
-// Measured: 4,096 rows of 5,120 with an fp32 residual and a gate per token in 54.1 us,
-// 5.4 TB/s (84 % of the copy rate; two vectors a thread, 320 threads); 256 rows in 5.3 us and 8 rows in
-// 3.9 us, which is the two barriers and a launch.
-#include <algorithm>
-
+// Measured: 4,096 rows of 5,120 with an fp32 residual and a gate per token in 52.9 us,
+// 5.6 TB/s (86 % of the copy rate; two vectors a thread, 320 threads); 256 rows in 5.0 us and 8 rows in
+// 4.1 us, which is the two barriers and a launch.
 #include "common.cuh"
 
 namespace dfl {
@@ -98,8 +96,8 @@ __device__ __forceinline__ float act(float g, int sigmoid) {
     return r;
 }
 
-// Sum over the block, the same value in every thread (`buf`: 32 floats, free
-// for the next call one barrier later).
+// Sum over the block, the same value in every thread (`buf`: 32 floats, to be used
+// again one barrier later).
 __device__ __forceinline__ float block_sum(float v, float* buf) {
 #pragma unroll
     for (int j = 16; j > 0; j >>= 1) v += __shfl_xor_sync(FULL, v, j);
@@ -116,76 +114,71 @@ __device__ __forceinline__ float block_sum(float v, float* buf) {
 // XT: y, gate, weights and h; RT: the residual; a thread holds V packs of W
 // elements of the row (blockDim V W >= H; W = 8 wants H a multiple of 8 and
 // 16-byte rows, W = 1 takes any).  Everything a row needs from memory is
-// requested before its first sum.
-// Two packs of 16-bit elements fit 64 registers (the compiler takes 94 of its own
-// accord), and with them three rows of 5,120 are in flight on an SM instead of two:
-// 63.6 -> 54.1 us; fp32 packs would spill, and one element at a time is slower when
-// it is told anything (7.2 -> 9.6 us at 1,001 x 1,023).
+// requested before its first sum.  A CTA takes one row: in a loop over rows the two
+// packs of 5,120 bf16 columns take 94 registers a thread and two rows fit an SM,
+// without it about 60 and three (63.6 and 52.9 us at 4,096 rows).
 template <typename XT, typename RT, int W, int V>
-__global__ void __launch_bounds__(512, W == 8 && V == 2 && sizeof(XT) == 2 ? 2 : 0)
-    norm_residual_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(512) norm_residual_kernel(const NormArgs a) {
     __shared__ float buf[2][32];
     const int np = (int)(a.H / W);
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        const XT* y = (const XT*)a.y + row * a.y_stride;
-        const RT* r = (const RT*)a.res + row * a.res_stride;
-        const XT* g = a.gate ? (const XT*)a.gate + row / a.gate_rep * a.gate_stride : nullptr;
-        Pack<XT, W> py[V], pg[V];
-        Pack<RT, W> pr[V];
-        float ss = 0.0f;
+    const int64_t row = blockIdx.x;
+    const XT* y = (const XT*)a.y + row * a.y_stride;
+    const RT* r = (const RT*)a.res + row * a.res_stride;
+    const XT* g = a.gate ? (const XT*)a.gate + row / a.gate_rep * a.gate_stride : nullptr;
+    Pack<XT, W> py[V], pg[V];
+    Pack<RT, W> pr[V];
+    float ss = 0.0f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int q = threadIdx.x + i * blockDim.x;
-            if (q < np) {
-                py[i].load(y + W * q);
-                pr[i].load(r + W * q);
-                if (g) pg[i].load(g + W * q);
+    for (int i = 0; i < V; ++i) {
+        const int q = threadIdx.x + i * blockDim.x;
+        if (q < np) {
+            py[i].load(y + W * q);
+            pr[i].load(r + W * q);
+            if (g) pg[i].load(g + W * q);
+        }
+    }
+    float inv = a.alpha;
+    if (a.w_post) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (threadIdx.x + i * blockDim.x < np)
+#pragma unroll
+                for (int e = 0; e < W; ++e) ss = fmaf(py[i].get(e), py[i].get(e), ss);
+        inv *= rsqrtf(block_sum(ss, buf[0]) / (float)a.H + a.eps);
+    }
+    float vr[V][W];
+    float s2 = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int q = threadIdx.x + i * blockDim.x;
+        if (q < np) {
+            Pack<XT, W> pw;
+            if (a.w_post) pw.load((const XT*)a.w_post + W * q);
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                float f = inv;
+                if (a.w_post) f *= pw.get(e) + a.w_offset;
+                if (g) f *= act(pg[i].get(e), a.sigmoid);
+                vr[i][e] = fmaf(f, py[i].get(e), pr[i].get(e));
+                s2 = fmaf(vr[i][e], vr[i][e], s2);
             }
+            store_pack((RT*)a.res_out + row * a.H + W * q, vr[i]);
         }
-        float inv = a.alpha;
-        if (a.w_post) {
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (threadIdx.x + i * blockDim.x < np)
-#pragma unroll
-                    for (int e = 0; e < W; ++e) ss = fmaf(py[i].get(e), py[i].get(e), ss);
-            inv *= rsqrtf(block_sum(ss, buf[0]) / (float)a.H + a.eps);
-        }
-        float vr[V][W];
-        float s2 = 0.0f;
+    }
+    if (a.w_pre) {
+        const float inv2 = rsqrtf(block_sum(s2, buf[1]) / (float)a.H + a.eps);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int q = threadIdx.x + i * blockDim.x;
             if (q < np) {
                 Pack<XT, W> pw;
-                if (a.w_post) pw.load((const XT*)a.w_post + W * q);
+                pw.load((const XT*)a.w_pre + W * q);
+                float o[W];
 #pragma unroll
-                for (int e = 0; e < W; ++e) {
-                    float f = inv;
-                    if (a.w_post) f *= pw.get(e) + a.w_offset;
-                    if (g) f *= act(pg[i].get(e), a.sigmoid);
-                    vr[i][e] = fmaf(f, py[i].get(e), pr[i].get(e));
-                    s2 = fmaf(vr[i][e], vr[i][e], s2);
-                }
-                store_pack((RT*)a.res_out + row * a.H + W * q, vr[i]);
+                for (int e = 0; e < W; ++e) o[e] = vr[i][e] * inv2 * (pw.get(e) + a.w_offset);
+                store_pack((XT*)a.h + row * a.H + W * q, o);
             }
         }
-        if (a.w_pre) {
-            const float inv2 = rsqrtf(block_sum(s2, buf[1]) / (float)a.H + a.eps);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int q = threadIdx.x + i * blockDim.x;
-                if (q < np) {
-                    Pack<XT, W> pw;
-                    pw.load((const XT*)a.w_pre + W * q);
-                    float o[W];
-#pragma unroll
-                    for (int e = 0; e < W; ++e) o[e] = vr[i][e] * inv2 * (pw.get(e) + a.w_offset);
-                    store_pack((XT*)a.h + row * a.H + W * q, o);
-                }
-            }
-        }
-        if (gridDim.x < a.rows) __syncthreads();  // the sums' buffers are used again
     }
 }
 
@@ -196,42 +189,40 @@ __global__ void __launch_bounds__(512, W == 8 && V == 2 && sizeof(XT) == 2 ? 2 :
 template <typename XT, typename RT>
 __global__ void __launch_bounds__(512) norm_residual_any_kernel(const NormArgs a) {
     __shared__ float buf[2][32];
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        const XT* y = (const XT*)a.y + row * a.y_stride;
-        const RT* r = (const RT*)a.res + row * a.res_stride;
-        const XT* g = a.gate ? (const XT*)a.gate + row / a.gate_rep * a.gate_stride : nullptr;
-        const XT* wpost = (const XT*)a.w_post;
-        const XT* wpre = (const XT*)a.w_pre;
-        float inv = a.alpha;
-        if (wpost) {
-            float ss = 0.0f;
-            for (int64_t i = threadIdx.x; i < a.H; i += blockDim.x) {
-                const float v = ld_1(y + i);
-                ss = fmaf(v, v, ss);
-            }
-            inv *= rsqrtf(block_sum(ss, buf[0]) / (float)a.H + a.eps);
+    const int64_t row = blockIdx.x;
+    const XT* y = (const XT*)a.y + row * a.y_stride;
+    const RT* r = (const RT*)a.res + row * a.res_stride;
+    const XT* g = a.gate ? (const XT*)a.gate + row / a.gate_rep * a.gate_stride : nullptr;
+    const XT* wpost = (const XT*)a.w_post;
+    const XT* wpre = (const XT*)a.w_pre;
+    float inv = a.alpha;
+    if (wpost) {
+        float ss = 0.0f;
+        for (int64_t i = threadIdx.x; i < a.H; i += blockDim.x) {
+            const float v = ld_1(y + i);
+            ss = fmaf(v, v, ss);
         }
-        auto sum_at = [&](int64_t i) {
-            float f = inv;
-            if (wpost) f *= ld_1(wpost + i) + a.w_offset;
-            if (g) f *= act(ld_1(g + i), a.sigmoid);
-            return fmaf(f, ld_1(y + i), ld_1(r + i));
-        };
-        float inv2 = 0.0f;
-        if (wpre) {
-            float s2 = 0.0f;
-            for (int64_t i = threadIdx.x; i < a.H; i += blockDim.x) {
-                const float v = sum_at(i);
-                s2 = fmaf(v, v, s2);
-            }
-            inv2 = rsqrtf(block_sum(s2, buf[1]) / (float)a.H + a.eps);
-        }
+        inv *= rsqrtf(block_sum(ss, buf[0]) / (float)a.H + a.eps);
+    }
+    auto sum_at = [&](int64_t i) {
+        float f = inv;
+        if (wpost) f *= ld_1(wpost + i) + a.w_offset;
+        if (g) f *= act(ld_1(g + i), a.sigmoid);
+        return fmaf(f, ld_1(y + i), ld_1(r + i));
+    };
+    float inv2 = 0.0f;
+    if (wpre) {
+        float s2 = 0.0f;
         for (int64_t i = threadIdx.x; i < a.H; i += blockDim.x) {
             const float v = sum_at(i);
-            st_1((RT*)a.res_out + row * a.H + i, v);
-            if (wpre) st_1((XT*)a.h + row * a.H + i, v * inv2 * (ld_1(wpre + i) + a.w_offset));
+            s2 = fmaf(v, v, s2);
         }
-        if (gridDim.x < a.rows) __syncthreads();
+        inv2 = rsqrtf(block_sum(s2, buf[1]) / (float)a.H + a.eps);
+    }
+    for (int64_t i = threadIdx.x; i < a.H; i += blockDim.x) {
+        const float v = sum_at(i);
+        st_1((RT*)a.res_out + row * a.H + i, v);
+        if (wpre) st_1((XT*)a.h + row * a.H + i, v * inv2 * (ld_1(wpre + i) + a.w_offset));
     }
 }
 
@@ -244,7 +235,7 @@ namespace {
 
 template <typename XT, typename RT>
 int launch(const NormArgs& a, bool vec, cudaStream_t s) {
-    const unsigned grid = (unsigned)std::min<int64_t>(a.rows, 1 << 30);
+    const unsigned grid = (unsigned)a.rows;  // at most 2^30
     // packs of a row; up to 512 threads take V of them each, all but evenly
     const int64_t np = vec ? a.H / 8 : a.H;
     auto threads = [&](int v) { return (int)(((np + v - 1) / v + 31) / 32 * 32); };
