@@ -10,9 +10,15 @@
 // by one CTA sized to it; rows too long for its registers are read again from
 // cache (three passes).
 //
-// Measured: 4,096 rows of 5,120 with an fp32 residual and a gate per token in 52.9 us,
-// 5.6 TB/s (86 % of the copy rate; two vectors a thread, 320 threads); 256 rows in 5.0 us and 8 rows in
-// 4.1 us, which is the two barriers and a launch.
+// Sums of squares that leave fp32's range are formed again from the row scaled by a
+// power of two, so finite rows of any size are right; no other row pays more than a test.
+//
+// Measured: 4,096 rows of 5,120 with an fp32 residual and a gate per token in 50 us,
+// 5.9 TB/s (91 % of the copy rate; two vectors a thread, 320 threads); 256 rows in 4.8 us and 8 rows in
+// 3.9 us, which is the two barriers and a launch; 1,001 rows of 6,001, by element in three
+// passes, in 40 us, 1.5 TB/s.
+#include <cfloat>
+
 #include "common.cuh"
 
 namespace dfl {
@@ -111,12 +117,31 @@ __device__ __forceinline__ float block_sum(float v, float* buf) {
     return v;
 }
 
+// Whether fp32 holds a mean square (with eps) in full: not where values lie beyond about
+// 1e19 / sqrt(H), nor where all lie below 1e-18 with no eps to cover them.
+__device__ __forceinline__ bool in_range(float m) { return m >= 0x1p-120f && m <= FLT_MAX; }
+
+// 1 / sqrt(sum / H + eps), `sum` a row's sum of squares.  Out of range, the row is summed
+// once more, `again(c)` the thread's sum of (c v)^2 with c a power of two that brings it
+// back; the whole block takes the same branch.
+template <typename Again>
+__device__ __forceinline__ float inv_rms(float sum, float H, float eps, float* buf, const Again& again) {
+    float m = sum / H + eps;
+    if (in_range(m)) return rsqrtf(m);
+    const float c = m > 1.0f ? 0x1p-80f : 0x1p100f;
+    __syncthreads();  // `buf` is read
+    m = block_sum(again(c), buf) / H + eps * c * c;
+    return c * rsqrtf(m);
+}
+
 // XT: y, gate, weights and h; RT: the residual; a thread holds V packs of W
 // elements of the row (blockDim V W >= H; W = 8 wants H a multiple of 8 and
-// 16-byte rows, W = 1 takes any).  Everything a row needs from memory is
-// requested before its first sum.  A CTA takes one row: in a loop over rows the two
-// packs of 5,120 bf16 columns take 94 registers a thread and two rows fit an SM,
-// without it about 60 and three (63.6 and 52.9 us at 4,096 rows).
+// 16-byte rows, W = 1 takes any).  A row's y, residual and gate are requested before
+// its first sum; the weights ahead of the sum before their use where they are at most 32
+// bytes a thread (requested behind it, 256 rows of 5,120 take 5.2 us instead of 4.8; with
+// more bytes ahead, 1,024 fp32 rows of 16,384 take 87 instead of 79).  A CTA takes one
+// row: in a loop over rows the two packs of 5,120 bf16 columns take 94 registers a thread
+// and two rows fit an SM, without it about 60 and three (63.6 and 52.9 us at 4,096 rows).
 template <typename XT, typename RT, int W, int V>
 __global__ void __launch_bounds__(512) norm_residual_kernel(const NormArgs a) {
     __shared__ float buf[2][32];
@@ -138,13 +163,30 @@ __global__ void __launch_bounds__(512) norm_residual_kernel(const NormArgs a) {
         }
     }
     float inv = a.alpha;
+    Pack<XT, W> pw[V];  // of w_post, then of w_pre
+    constexpr bool EARLY = V * W * sizeof(XT) <= 32;
+    auto load_w = [&](const void* w, int i) {
+        const int q = threadIdx.x + i * blockDim.x;
+        if (q < np) pw[i].load((const XT*)w + W * q);
+    };
     if (a.w_post) {
+        if (EARLY)
+#pragma unroll
+            for (int i = 0; i < V; ++i) load_w(a.w_post, i);
 #pragma unroll
         for (int i = 0; i < V; ++i)
             if (threadIdx.x + i * blockDim.x < np)
 #pragma unroll
                 for (int e = 0; e < W; ++e) ss = fmaf(py[i].get(e), py[i].get(e), ss);
-        inv *= rsqrtf(block_sum(ss, buf[0]) / (float)a.H + a.eps);
+        inv *= inv_rms(block_sum(ss, buf[0]), (float)a.H, a.eps, buf[0], [&](float c) {
+            float t = 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (threadIdx.x + i * blockDim.x < np)
+#pragma unroll
+                    for (int e = 0; e < W; ++e) t = fmaf(c * py[i].get(e), c * py[i].get(e), t);
+            return t;
+        });
     }
     float vr[V][W];
     float s2 = 0.0f;
@@ -152,12 +194,11 @@ __global__ void __launch_bounds__(512) norm_residual_kernel(const NormArgs a) {
     for (int i = 0; i < V; ++i) {
         const int q = threadIdx.x + i * blockDim.x;
         if (q < np) {
-            Pack<XT, W> pw;
-            if (a.w_post) pw.load((const XT*)a.w_post + W * q);
+            if (!EARLY && a.w_post) load_w(a.w_post, i);
 #pragma unroll
             for (int e = 0; e < W; ++e) {
                 float f = inv;
-                if (a.w_post) f *= pw.get(e) + a.w_offset;
+                if (a.w_post) f *= pw[i].get(e) + a.w_offset;
                 if (g) f *= act(pg[i].get(e), a.sigmoid);
                 vr[i][e] = fmaf(f, py[i].get(e), pr[i].get(e));
                 s2 = fmaf(vr[i][e], vr[i][e], s2);
@@ -166,43 +207,67 @@ __global__ void __launch_bounds__(512) norm_residual_kernel(const NormArgs a) {
         }
     }
     if (a.w_pre) {
-        const float inv2 = rsqrtf(block_sum(s2, buf[1]) / (float)a.H + a.eps);
+        if (EARLY)
+#pragma unroll
+            for (int i = 0; i < V; ++i) load_w(a.w_pre, i);
+        const float inv2 = inv_rms(block_sum(s2, buf[1]), (float)a.H, a.eps, buf[1], [&](float c) {
+            float t = 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (threadIdx.x + i * blockDim.x < np)
+#pragma unroll
+                    for (int e = 0; e < W; ++e) t = fmaf(c * vr[i][e], c * vr[i][e], t);
+            return t;
+        });
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int q = threadIdx.x + i * blockDim.x;
             if (q < np) {
-                Pack<XT, W> pw;
-                pw.load((const XT*)a.w_pre + W * q);
+                if (!EARLY) load_w(a.w_pre, i);
                 float o[W];
 #pragma unroll
-                for (int e = 0; e < W; ++e) o[e] = vr[i][e] * inv2 * (pw.get(e) + a.w_offset);
+                for (int e = 0; e < W; ++e) o[e] = vr[i][e] * inv2 * (pw[i].get(e) + a.w_offset);
                 store_pack((XT*)a.h + row * a.H + W * q, o);
             }
         }
     }
 }
 
-// Any width, stride and alignment: element by element, y and r read again from
-// cache after each sum.  r' is recomputed in the last pass, not read back, so
-// that h comes from the unrounded value; where the output is written over the
-// residual, r' of a row is written only after its last read.
-template <typename XT, typename RT>
-__global__ void __launch_bounds__(512) norm_residual_any_kernel(const NormArgs a) {
-    __shared__ float buf[2][32];
-    const int64_t row = blockIdx.x;
+// A row of any width, stride and alignment: element by element, y and r read again from
+// cache after each sum.  r' is recomputed in the last pass, not read back, so that h comes
+// from the unrounded value; where the output is written over the residual, r' is written
+// only after its last read.  A row with a sum out of range returns false, with nothing
+// written, unless SCALED, which takes such a sum once more of c v.
+template <typename XT, typename RT, bool SCALED>
+__device__ __forceinline__ bool row_by_element(const NormArgs& a, int64_t row, float* buf) {
+    constexpr int U = SCALED ? 1 : 4;  // loads in flight
     const XT* y = (const XT*)a.y + row * a.y_stride;
     const RT* r = (const RT*)a.res + row * a.res_stride;
     const XT* g = a.gate ? (const XT*)a.gate + row / a.gate_rep * a.gate_stride : nullptr;
     const XT* wpost = (const XT*)a.w_post;
     const XT* wpre = (const XT*)a.w_pre;
+    // 1 / sqrt(mean square + eps) of value(0) .. value(H - 1), or 0 for out of range
+    auto inv_rms = [&](float* buf, auto&& value) {
+        float c = 1.0f;
+        for (;;) {
+            float t = 0.0f;
+#pragma unroll U
+            for (int64_t i = threadIdx.x; i < a.H; i += blockDim.x) {
+                const float v = SCALED ? c * value(i) : value(i);
+                t = fmaf(v, v, t);
+            }
+            if (SCALED) __syncthreads();  // `buf` is read
+            const float m = block_sum(t, buf) / (float)a.H + (SCALED ? a.eps * c * c : a.eps);
+            if (!SCALED) return in_range(m) ? rsqrtf(m) : 0.0f;
+            if (in_range(m) || c != 1.0f) return c * rsqrtf(m);
+            c = m > 1.0f ? 0x1p-80f : 0x1p100f;
+        }
+    };
     float inv = a.alpha;
     if (wpost) {
-        float ss = 0.0f;
-        for (int64_t i = threadIdx.x; i < a.H; i += blockDim.x) {
-            const float v = ld_1(y + i);
-            ss = fmaf(v, v, ss);
-        }
-        inv *= rsqrtf(block_sum(ss, buf[0]) / (float)a.H + a.eps);
+        const float f = inv_rms(buf, [&](int64_t i) { return ld_1(y + i); });
+        if (!SCALED && f == 0.0f) return false;
+        inv *= f;
     }
     auto sum_at = [&](int64_t i) {
         float f = inv;
@@ -212,18 +277,21 @@ __global__ void __launch_bounds__(512) norm_residual_any_kernel(const NormArgs a
     };
     float inv2 = 0.0f;
     if (wpre) {
-        float s2 = 0.0f;
-        for (int64_t i = threadIdx.x; i < a.H; i += blockDim.x) {
-            const float v = sum_at(i);
-            s2 = fmaf(v, v, s2);
-        }
-        inv2 = rsqrtf(block_sum(s2, buf[1]) / (float)a.H + a.eps);
+        inv2 = inv_rms(buf + 32, sum_at);
+        if (!SCALED && inv2 == 0.0f) return false;
     }
+#pragma unroll U
     for (int64_t i = threadIdx.x; i < a.H; i += blockDim.x) {
         const float v = sum_at(i);
         st_1((RT*)a.res_out + row * a.H + i, v);
         if (wpre) st_1((XT*)a.h + row * a.H + i, v * inv2 * (ld_1(wpre + i) + a.w_offset));
     }
+    return true;
+}
+template <typename XT, typename RT>
+__global__ void __launch_bounds__(512) norm_residual_any_kernel(const __grid_constant__ NormArgs a) {
+    __shared__ float buf[64];
+    if (!row_by_element<XT, RT, false>(a, blockIdx.x, buf)) row_by_element<XT, RT, true>(a, blockIdx.x, buf);
 }
 
 }  // namespace dfl

@@ -527,8 +527,10 @@ DFLASH2_API int dflash2_dynconv2_w4(const void* x, const void* x_prev, const voi
  * h           [rows, H] of `dtype`, dense.
  * H a multiple of 8, at most 16,384, with rows that start on 16 bytes is read
  * with 128-bit loads in one pass; other shapes element by element.  No
- * workspace.  A row's bits do not depend on the other rows.  Squares are summed in
- * fp32: a row with values beyond 1e18 overflows it.
+ * workspace.  A row's bits do not depend on the other rows.  Finite rows of any size
+ * are right (a sum of squares that leaves fp32 is formed again from the row scaled by a
+ * power of two), as long as r' and 1 / sqrt(mean + eps) times the factors beside it are
+ * fp32 numbers: with eps 0, down to a root mean square of about 1e-38.
  */
 #define DFLASH2_GATE_LINEAR 0
 #define DFLASH2_GATE_SIGMOID 1

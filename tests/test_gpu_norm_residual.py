@@ -234,3 +234,60 @@ def test_capture_and_streams():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, ref))
         assert all(torch.equal(a, b) for a, b in zip(eager, want2))
+
+
+def compare_denormal(got, want, d, H, eps):
+    """compare()'s bound where values below 2^-126 are steps of 2^-149 (bf16: 2^-133): an
+    fp32 result that small is off by at most 2^-150 (r' by one such rounding, h by that of
+    v / rms, times w, and of the product), an output of bf16 by 2^-134 more.  A row's
+    reciprocal below 2^-126 (rms above 2^126) is off by 2^-150 of at least 2^-128.2, so 2.3
+    steps of 2^-24; it and its products with w and the gate, 7 steps, fit in E, whose
+    terms add up to H / 1024 + 38 of its H / 512 + 70 steps."""
+    r, h = got if isinstance(got, tuple) else (got, None)
+    rr, hh = want
+    E = (H / 512 + 70) * 2.0 ** -24
+    branch = np.abs(rr - f64(d["res"]))
+    er = E * branch + 2.0 ** -24 * (np.abs(rr) + branch) + 2.0 ** -150
+    tol = er + (2.0 ** -8 * (np.abs(rr) + er) + 2.0 ** -134 if r.dtype == torch.bfloat16 else 0.0)
+    err = np.abs(f64(r) - rr)
+    assert (err <= tol).all(), ("r'", (err / tol).max(-1))
+    if hh is None:
+        return
+    scale = 1 / np.sqrt((rr ** 2).mean(-1, keepdims=True) + eps)
+    w = np.abs(f64(d["w_pre"]))
+    eh = w * scale * er + np.abs(hh) * (E + (er * np.abs(rr)).mean(-1, keepdims=True) * scale ** 2) + \
+        (w + 1) * 2.0 ** -150
+    tol = eh + (2.0 ** -8 * (np.abs(hh) + eh) + 2.0 ** -134 if h.dtype == torch.bfloat16 else 0.0)
+    err = np.abs(f64(h) - hh)
+    assert (err <= tol).all(), ("h", (err / tol).max(-1))
+
+
+@pytest.mark.parametrize("dt,rdt", TYPES)
+@pytest.mark.parametrize("H", [8, 31, 264, 1023, 5120, 6001, 8200, 16384, 20000])
+def test_squares_beyond_fp32(orc, dt, rdt, H):
+    """Finite rows whose squares (or their sum alone) leave fp32: the same bound as any
+    other row's.  Rows far below one are taken with eps = 0, where eps does not cover them."""
+    need_cuda()
+    rng = np.random.default_rng(H)
+    rows = 8
+    d = inputs(rng, 1, rows, H, "f32", "f32", "none", True, True)
+    flat = lambda size: rng.choice([-1.0, 1.0], H) * rng.uniform(0.5, 1.0, H) * size
+    d["y"][0, 0] = flat(3e38)
+    d["y"][0, 1] = flat(1.8e19)              # each square fits, a few of them do not
+    d["y"][0, 2] = flat(4e37) * (np.arange(H) == H - 1)   # one element alone
+    d["res"][0, 3] = flat(3e38)
+    d["res"][0, 4] = flat(1e20)
+    d["y"][0, 5] = flat(2e25)
+    d["res"][0, 5] = flat(2e25)
+    low = {k: None if v is None else v.copy() for k, v in d.items()}
+    for i, size in enumerate([1e-19, 1e-21, 1e-25, 1e-30, 1e-36]):
+        low["y"][0, i] = flat(size)
+        low["res"][0, i] = flat(1e-30)
+    for case, eps in ((d, 1e-6), (low, 0.0), (low, 1e-44)):
+        for post, pre in ((True, True), (False, True), (True, False)):
+            c = dict(case, w_post=case["w_post"] if post else None, w_pre=case["w_pre"] if pre else None)
+            if dt == "bf16":
+                c = {k: v if v is None or (k == "res" and rdt == "f32") else synth.to_bf16_bits(v) for k, v in c.items()}
+            got = dfl.norm_residual(**dev(c), eps=eps)
+            want = oracle(orc, c, 1, rows, H, eps=float(np.float32(eps)))
+            compare_denormal(got, want, c, H, float(np.float32(eps)))
