@@ -457,9 +457,9 @@ def linear_w4(x, w4, out_dtype=None, out=None):
     dx = _dtype(x)
     x2, stride = (x, K) if x.is_contiguous() else _rows(x, K)
     rows = x.numel() // K
-    if rows > 16 and not x.is_contiguous() and (x2.data_ptr() | stride * x.element_size()) & 15:
+    if rows > 16 and (x2.data_ptr() | stride * x2.element_size()) & 15:
         # rows that do not start on 16 bytes: the tensor cores' copies want them to
-        x2, stride = x2.contiguous(), K
+        x2, stride = x2.clone(memory_format=torch.contiguous_format), K
     oshape = shape[:-1] + (N,)
     if out is None:
         out = x.new_empty(oshape, dtype=out_dtype)

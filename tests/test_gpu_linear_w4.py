@@ -370,3 +370,24 @@ def test_large_activations_on_zero_points_leave_no_trace(orc, group, zeros, f32_
     ref, mag = orc.dynconv2_w4(x, xp, q, s, z)
     assert_within(f64(out), ref, mag, K, 1, True, "conv", factor=1.0 + 2 / 34)
     assert dfl.device_errors() == 0
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_dense_rows_off_16_bytes(orc, dt):
+    """A dense x whose storage starts anywhere goes the way of an aligned copy, strided or not."""
+    need_cuda()
+    rng = np.random.default_rng(23)
+    N, K = 200, 1024
+    q, s, z = weights(rng, N, K, 64, True)
+    w = packed(q, s, z)
+    for tokens in (3, 16, 17, 20, 140):
+        x = activations(rng, (tokens, K), dt)
+        flat = torch.zeros(tokens * K + 9, dtype=torch.bfloat16 if dt == "bf16" else torch.float32, device="cuda")
+        for off in (0, 1, 3, 8):
+            v = flat[off:off + tokens * K].view(tokens, K)
+            v.copy_(to_dev(x))
+            assert v.is_contiguous()
+            y = dfl.linear_w4(v, w, out_dtype=torch.float32)
+            assert torch.equal(y, dfl.linear_w4(to_dev(x), w, out_dtype=torch.float32)), (tokens, off)
+        ref, mag = orc.linear_w4(x, q, s, z)
+        assert_within(f64(y), ref, mag, K, 3 if dt == "f32" else 1, False, "dense")
