@@ -73,6 +73,7 @@ def lib():
         L.dflash2_w4_packed_bytes.restype = sz
         L.dflash2_w4_pack.argtypes = [vp, vp, vp, i64, i64, i32, i32, vp, vp]
         L.dflash2_linear_w4.argtypes = [vp, i32, i64, i64, vp, i64, i64, i32, i32, vp, i32, vp]
+        L.dflash2_linear_w4_plan.argtypes = [i64, i64, i64, i32, i32, i32, C.POINTER(i32), C.POINTER(i32)]
         L.dflash2_dynconv2_w4.argtypes = [vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp]
         L.dflash2_norm_residual.argtypes = [vp, i32, i64, vp, i32, i64, vp, i64, i64, i32, vp, vp,
                                             f32, f32, f32, i64, i64, vp, vp, vp]
@@ -83,7 +84,7 @@ def lib():
                   "dflash2_verify_greedy", "dflash2_verify_sample", "dflash2_verify_sample_ex",
                   "dflash2_verify_sample_trunc", "dflash2_dynconv2", "dflash2_dynconv2_pack",
                   "dflash2_dynconv2_packed", "dflash2_w4_pack", "dflash2_linear_w4",
-                  "dflash2_dynconv2_w4", "dflash2_norm_residual"):
+                  "dflash2_linear_w4_plan", "dflash2_dynconv2_w4", "dflash2_norm_residual"):
             getattr(L, f).restype = i32
         _lib = L
     return _lib

@@ -679,12 +679,10 @@ int launch_any(const W4Args& a, const W4Plan& P, int format, bool x_f32, int dev
 constexpr int W4_FORMATS = DFLASH2_W4_ZERO | DFLASH2_W4_SCALE_F32 | DFLASH2_W4_TAPS;
 constexpr int64_t W4_MAX_TOKENS = 1 << 18;
 
-// A checked call: by token count and type to one of the two kernels.
-int run(const W4Call& c, cudaStream_t s) {
-    W4Dev d;
-    if (!device_info(d)) return DFLASH2_ECUDA;
+// The plan of the few-token kernel, or NULL where the call goes to the tensor cores.
+const W4Plan* few_plan(const W4Call& c, const W4Dev& d) {
     const bool tc = dfl_linear_w4_tc_ok(c);
-    if (tc && c.tokens > W4_FEW_TOKENS) return dfl_linear_w4_tc(c, d, s);
+    if (tc && c.tokens > W4_FEW_TOKENS) return nullptr;
     // the plan of the thread's last shape is kept: a decode calls the same ones over
     struct Last {
         int64_t N, K, tokens;
@@ -696,8 +694,16 @@ int run(const W4Call& c, cudaStream_t s) {
         last.format != c.format || last.x_f32 != c.x_f32 || last.dev != d.id)
         last = {c.L.N, c.L.K, c.tokens, c.L.group, c.format, c.x_f32, d.id,
                 w4_plan(c.L, c.format, c.tokens, c.x_f32, d)};
-    const W4Plan& P = last.P;
-    if (tc && c.tokens > 8 && P.phases > 2) return dfl_linear_w4_tc(c, d, s);
+    return tc && c.tokens > 8 && last.P.phases > 2 ? nullptr : &last.P;
+}
+
+// A checked call: by token count and type to one of the two kernels.
+int run(const W4Call& c, cudaStream_t s) {
+    W4Dev d;
+    if (!device_info(d)) return DFLASH2_ECUDA;
+    const W4Plan* few = few_plan(c, d);
+    if (!few) return dfl_linear_w4_tc(c, d, s);
+    const W4Plan& P = *few;
     W4Args a{};
     a.packed = (const uint8_t*)c.packed;
     a.N = c.L.N;
@@ -775,6 +781,30 @@ extern "C" int dflash2_linear_w4(const void* x, int dtype, int64_t x_stride, int
     c.y = y;
     c.y_bf16 = out_dtype == DFLASH2_BF16;
     return run(c, (cudaStream_t)stream);
+}
+
+extern "C" int dflash2_linear_w4_plan(int64_t tokens, int64_t N, int64_t K, int group, int format,
+                                      int dtype, int* tile, int* cluster) {
+    if (!dtype_ok(dtype)) return DFLASH2_EDTYPE;
+    if (format < 0 || (format & ~W4_FORMATS) || !tile || !cluster) return DFLASH2_EINVAL;
+    if (!w4_shape_ok(N, K, group) || tokens < 1 || tokens > W4_MAX_TOKENS) return DFLASH2_ESHAPE;
+    W4Dev d;
+    if (!device_info(d)) return DFLASH2_ECUDA;
+    W4Call c{};
+    c.L = w4_layout(N, K, group, format);
+    c.format = format & ~DFLASH2_W4_TAPS;
+    c.tokens = tokens;
+    c.x_f32 = dtype == DFLASH2_F32;
+    c.x_vec = true;
+    if (const W4Plan* few = few_plan(c, d)) {
+        *tile = 0;
+        *cluster = few->S;
+    } else {
+        const W4TcPlan P = dfl_linear_w4_tc_plan(c, d);
+        *tile = P.ntok;
+        *cluster = P.S;
+    }
+    return DFLASH2_OK;
 }
 
 extern "C" int dflash2_dynconv2_w4(const void* x, const void* x_prev, const void* packed, int group,

@@ -32,5 +32,13 @@ struct W4Dev {
 // 9; 5,120 x 20,480 (x in four parts), 22.6 and 37.0 at 8, 83.5 and 37.1 at 9.
 constexpr int64_t W4_FEW_TOKENS = 16;
 
+// Tiles of the tensor-core kernel: tokens per tile and tiles of tokens, cluster size,
+// clusters, tiles.
+struct W4TcPlan {
+    int ntok, tt, S, C;
+    int64_t tiles;
+};
+
 bool dfl_linear_w4_tc_ok(const W4Call& c);
+W4TcPlan dfl_linear_w4_tc_plan(const W4Call& c, const W4Dev& d);
 int dfl_linear_w4_tc(const W4Call& c, const W4Dev& d, cudaStream_t s);

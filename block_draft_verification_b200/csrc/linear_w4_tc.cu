@@ -54,7 +54,7 @@ constexpr int TW_NA = 4;                // chunks in the operand rings (A and x)
 
 struct W4TcArgs {
     const uint8_t* packed;
-    int64_t units, tokens, n_rows;  // n_rows: rows of W
+    int64_t tokens, n_rows;         // n_rows: rows of W
     int64_t ld;                     // linear: N; conv: H
     int steps, S, C, tt;            // K steps, cluster size, clusters, token tiles
     int64_t tiles;
@@ -757,29 +757,16 @@ bool dfl_linear_w4_tc_ok(const W4Call& c) {
     return c.x_vec && !c.x_f32 && encode_fn() != nullptr;
 }
 
-int dfl_linear_w4_tc(const W4Call& c, const W4Dev& d, cudaStream_t s) {
+// Tokens per tile and cluster size: rounds of tiles times the length of one, in
+// cycles.  A chunk takes about 300 for its barriers and codes and, per group, 250,
+// 370 or 690 for the sums of 32, 64 or 128 tokens (its MMAs and its weights'
+// share of memory bandwidth are below that); each round of a tile's end about 1,500,
+// 6,500 where sums cross CTAs.  (10,240 x 5,120: 23.9, 24.9 and 32.8 us at
+// 32, 64 and 128 tokens in groups of 128; 20,480 x 5,120 in groups of 64: 46, 50
+// and 95 us.)
+W4TcPlan dfl_linear_w4_tc_plan(const W4Call& c, const W4Dev& d) {
     const W4Layout& L = c.L;
-    W4TcArgs a{};
-    a.packed = (const uint8_t*)c.packed;
-    a.units = L.units;
-    a.tokens = c.tokens;
-    a.n_rows = L.N;
-    a.ld = c.x_prev ? L.K : L.N;
-    a.steps = L.steps;
-    a.y = c.y;
-    a.y_bf16 = c.y_bf16;
-    a.y_vec = L.N % 4 == 0 && (uintptr_t)c.y % 16 == 0;
-    a.x = (const __nv_bfloat16*)c.x;
-    a.x_prev = (const __nv_bfloat16*)c.x_prev;
-    a.T = c.T;
-    // Tokens per tile and cluster size: rounds of tiles times the length of one, in
-    // cycles.  A chunk takes about 300 for its barriers and codes and, per group, 250,
-    // 370 or 690 for the sums of 32, 64 or 128 tokens (its MMAs and its weights'
-    // share of memory bandwidth are below that); each round of a tile's end about 1,500,
-    // 6,500 where sums cross CTAs.  (10,240 x 5,120: 23.9, 24.9 and 32.8 us at
-    // 32, 64 and 128 tokens in groups of 128; 20,480 x 5,120 in groups of 64: 46, 50
-    // and 95 us.)
-    int ntok = 0;
+    W4TcPlan P{};
     int64_t best = -1;
     for (int n : {32, 64, 128}) {
         const int tt = (int)((c.tokens + n - 1) / n);
@@ -792,26 +779,44 @@ int dfl_linear_w4_tc(const W4Call& c, const W4Dev& d, cudaStream_t s) {
                                                           ends * (S > 1 ? 6500 : 1500));
             if (best < 0 || cost < best) {
                 best = cost;
-                ntok = n;
-                a.S = S;
-                a.C = (int)C;
-                a.tt = tt;
-                a.tiles = tiles;
+                P = {n, tt, S, (int)C, tiles};
             }
         }
     }
+    return P;
+}
+
+int dfl_linear_w4_tc(const W4Call& c, const W4Dev& d, cudaStream_t s) {
+    const W4Layout& L = c.L;
+    const W4TcPlan P = dfl_linear_w4_tc_plan(c, d);
+    W4TcArgs a{};
+    a.packed = (const uint8_t*)c.packed;
+    a.tokens = c.tokens;
+    a.n_rows = L.N;
+    a.ld = c.x_prev ? L.K : L.N;
+    a.steps = L.steps;
+    a.y = c.y;
+    a.y_bf16 = c.y_bf16;
+    a.y_vec = L.N % 4 == 0 && (uintptr_t)c.y % 16 == 0;
+    a.x = (const __nv_bfloat16*)c.x;
+    a.x_prev = (const __nv_bfloat16*)c.x_prev;
+    a.T = c.T;
+    a.S = P.S;
+    a.C = P.C;
+    a.tt = P.tt;
+    a.tiles = P.tiles;
     CUtensorMap map;
     cuuint64_t dims[2] = {(cuuint64_t)L.K, (cuuint64_t)c.tokens};
     cuuint64_t strides[1] = {(cuuint64_t)(c.tokens > 1 ? c.x_stride : L.K) * 2};
-    cuuint32_t box[2] = {W4_CHUNK, (cuuint32_t)ntok};
+    cuuint32_t box[2] = {W4_CHUNK, (cuuint32_t)P.ntok};
     cuuint32_t estr[2] = {1, 1};
     if (encode_fn()(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(c.x), dims, strides,
                     box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return DFLASH2_ECUDA;
-    if (ntok == 32) return launch_fmt<32>(map, a, L, c.format, d.id, s);
-    if (ntok == 64) return launch_fmt<64>(map, a, L, c.format, d.id, s);
+    if (P.ntok == 32) return launch_fmt<32>(map, a, L, c.format, d.id, s);
+    if (P.ntok == 64) return launch_fmt<64>(map, a, L, c.format, d.id, s);
     return launch_fmt<128>(map, a, L, c.format, d.id, s);
 }
 

@@ -65,7 +65,9 @@
  *   - Results are deterministic: a sequence's outputs depend only on its own
  *     inputs (and seq_id), not on the batch it runs in or on B -- except that
  *     dflash2_pair_select picks its implementation by B (see
- *     dflash2_pair_select_ex, which fixes it).
+ *     dflash2_pair_select_ex, which fixes it), and the products with 4-bit
+ *     weights their kernel and tiles by the number of tokens (see
+ *     dflash2_linear_w4_plan).
  */
 #ifndef DFLASH2_H
 #define DFLASH2_H
@@ -485,6 +487,16 @@ DFLASH2_API int dflash2_w4_pack(const uint8_t* q, const void* scale, const uint8
 DFLASH2_API int dflash2_linear_w4(const void* x, int dtype, int64_t x_stride, int64_t tokens,
                                   const void* packed, int64_t N, int64_t K, int group, int format,
                                   void* y, int out_dtype, dflash2_stream_t stream);
+
+/*
+ * The kernel that dflash2_linear_w4 (or, with N = 2H and K = H, dflash2_dynconv2_w4)
+ * runs for a shape on the current device, with rows of x that start on 16 bytes:
+ * *tile = the tokens of a tile on the tensor cores (32, 64 or 128), or 0 for the
+ * few-token kernel; *cluster = the CTAs that share a tile's K.  Calls with equal
+ * answers may still sum in another order.  Nothing is launched.
+ */
+DFLASH2_API int dflash2_linear_w4_plan(int64_t tokens, int64_t N, int64_t K, int group, int format,
+                                       int dtype, int* tile, int* cluster);
 
 /*
  * dflash2_dynconv2 with the tap weights in 4 bits: a quarter of the memory and, at

@@ -102,3 +102,17 @@ def test_binding_refuses_host_tensors(L):
     import block_draft_verification_b200 as d
     with pytest.raises(ValueError):
         d.PackedW4(torch.zeros((32, 32), dtype=torch.uint8), torch.ones((32, 2)))
+
+
+def test_plan_validation(L):
+    t, c = C.c_int(), C.c_int()
+    def plan(tok=8, N=128, K=128, g=128, fmt=0, dt=1, tile=C.byref(t), cl=C.byref(c)):
+        return L.dflash2_linear_w4_plan(tok, N, K, g, fmt, dt, tile, cl)
+    assert plan(tok=0) == ESHAPE
+    assert plan(tok=2 ** 18 + 1) == ESHAPE
+    assert plan(K=100) == ESHAPE
+    assert plan(g=48) == ESHAPE
+    assert plan(fmt=8) == EINVAL
+    assert plan(dt=7) == EDTYPE
+    assert plan(tile=None) == EINVAL
+    assert plan(cl=None) == EINVAL
