@@ -21,10 +21,10 @@
 // asynchronous copies; a lane copies and reads its own pieces only, so the
 // stream needs no barrier.
 //
-// Measured (8 tokens, groups of 128, bf16): 151,936 x 5,120 in 86 us, 4.7 TB/s of
-// packed weights; the logic pipe, which turns and masks the codes (5.5 operations a
-// word), is 60 % busy and 2.1 of 4 issue slots a cycle are taken, so the codes bound
-// it before memory does.  5,120 x 5,120 with one token: 8.7 us, of which the stream is
+// Measured (8 tokens, groups of 128, bf16): 151,936 x 5,120 in 92 us, 4.4 TB/s of
+// packed weights; the codes bound it before memory does: eight of them take three turns,
+// four masks and four subtractions, 2.4 of 4 issue slots a cycle are taken and the logic
+// pipe is 56 % busy.  5,120 x 5,120 with one token: 8.7 to 9.0 us, of which the stream is
 // a third: x is laid out first and the cluster's sums joined last.
 // More tokens than 16 go to linear_w4_tc.cu (bf16 activations).
 #include <cooperative_groups.h>
@@ -84,13 +84,6 @@ __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(a));
-    return v;
-}
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");

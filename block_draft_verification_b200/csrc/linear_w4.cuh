@@ -27,9 +27,11 @@ struct W4Dev {
 
 // The tensor-core kernel takes more than this many tokens, and fewer (above 8) where
 // the other kernel would have to fill its shared memory with x more than twice over.
-// Other kernel and this one: 10,240 x 5,120, 13.6 and 23.2 us at 8 tokens, 20.9 and
-// 23.4 at 16, 51.5 and 23.7 at 17; 20,480 x 5,120 (x in two parts), 27.7 and 43.4 at
-// 9; 5,120 x 20,480 (x in four parts), 22.6 and 37.0 at 8, 83.5 and 37.1 at 9.
+// Other kernel and this one: 10,240 x 5,120, 14.0 and 21.4 us at 8 tokens, 21.7 and
+// 21.6 at 16, 47.8 and 22.0 at 17; 20,480 x 5,120 (x in two parts), 34.4 and 37.5 at
+// 9, 39.7 and 37.8 at 16; 5,120 x 20,480 (x in four parts), 26.1 and 36.1 at 8, 84.0
+// and 36.2 at 9.  (At 16 tokens this one is also ahead at 5,120 x 5,120, 14.7 against
+// 16.9, and at 151,936 x 5,120, 161 against 202.)
 constexpr int64_t W4_FEW_TOKENS = 16;
 
 // Tiles of the tensor-core kernel: tokens per tile and tiles of tokens, cluster size,

@@ -89,6 +89,13 @@ __host__ __device__ inline int64_t w4_block(int64_t unit, int steps, int step, i
     return (((unit >> 2) * steps + step) * 4 + (unit & 3)) * step_bytes;
 }
 
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(a));
+    return v;
+}
 __device__ __forceinline__ uint32_t w4_turn(uint32_t w, int bits) {
     return bits == 0 ? w : __funnelshift_r(w, w, bits);
 }

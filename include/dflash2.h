@@ -477,7 +477,9 @@ DFLASH2_API int dflash2_w4_pack(const uint8_t* q, const void* scale, const uint8
  * y           [tokens, N] of `out_dtype`, dense.
  * The codes minus their zero points are multiplied exactly (fp32 activations
  * as three bf16 parts that add up to the value), sums are fp32, with one
- * rounding at a bf16 output; |x| below 2^-100 may lose its last bits.  A
+ * rounding at a bf16 output; |x| below 2^-100 may lose its last bits.  A group's
+ * scale multiplies the group's sum, so that sum (of codes up to 15 in magnitude times
+ * x) has to fit fp32 by itself: |x| below 1e37 / group always does.  A
  * NaN or an infinity in x leaves its token without a finite output (NaN, where
  * infinities may meet with either sign) and touches no other token.  A given
  * shape on a given device always rounds the same way; a token's last bits may
@@ -511,9 +513,9 @@ DFLASH2_API int dflash2_dynconv2_w4(const void* x, const void* x_prev, const voi
                                     void* out, dflash2_stream_t stream);
 
 /*
- * The norms around a block, fused with the block's gate and residual scale
- * ([tamsi] "L’idée, sans le papier": the convs sit before and after each
- * attention and MLP of the drafter, next to its norms).  For every row:
+ * The norms around a block, fused with the block's gate and residual scale.  Where
+ * a conv stands between the residual sum and the next norm, the first of them is
+ * used alone (w_pre NULL).  For every row:
  *
  *   r' = res + alpha * act(gate) * rms(y; w_post),   h = rms(r'; w_pre),
  *   rms(v; w)_i = v_i / sqrt(mean_j v_j^2 + eps) * (w_i + w_offset)
